@@ -313,6 +313,98 @@ bq_status bq_linear_grad_input(const void *dy, bq_dtype dtype, int64_t M, int64_
                                bq_layout layout, void *dx, void *stream);
 
 /*
+ * bq_dropout: out = mask * x / (1 - p), the mask drawn from a counter-based
+ * generator and never stored.  The same call on dy gives the gradient: the
+ * mask depends on (seed, offset, row, column) alone.
+ *   x, out   [rows, cols] of dtype (BQ_F16, BQ_BF16 or BQ_F32), row strides
+ *            ldx, ldo >= cols in elements; out may be x with ldo = ldx
+ *            (no other overlap).  Any column count and alignment of whole
+ *            elements; 16-byte aligned rows are the fast path.
+ *   p        probability of dropping an element, 0 <= p < 1, rounded to a
+ *            multiple of 2^-16 (1 - 2^-17 and above: BQ_ERR_UNSUPPORTED)
+ *   rng      DEVICE array {seed, offset}, read by the kernel, so that a captured
+ *            graph draws other masks when the values change between replays.
+ *            NULL is allowed when p rounds to 0.
+ * Generator: Philox 4x32-10 with key = seed and counter = (column / 8, row,
+ * offset) gives 128 bits for 8 columns; element j takes 16-bit field j % 8
+ * (least significant first) and is kept where the field is >= round(p 65536).
+ * A dropped element is 0 whatever x holds; a kept one is x * (65536 / (65536 -
+ * round(p 65536))) in fp32, rounded once (p = 0: x unchanged).
+ */
+bq_status bq_dropout(const void *x, bq_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, double p,
+                     const uint64_t *rng, void *out, int64_t ldo, void *stream);
+
+/*
+ * Low-rank adapters beside a shared projection.  The weight-only linear layer
+ * gives base = x . dequant(W)^T for every row; an adapter a adds
+ * s_a (drop(x) A_a^T) B_a^T for the rows of its requests.  The rows are
+ * grouped into S segments (serving: the rows of one request; training: the
+ * rows trained on one adapter):
+ *   seg_off      DEVICE int32 [S + 1], ascending: segment i is rows
+ *                [seg_off[i], seg_off[i + 1]) (may be empty).  Rows behind the
+ *                last segment are neither read nor written.
+ *   seg_adapter  DEVICE int32 [S]: the segment's adapter in 0 .. L - 1, or -1
+ *                for none.  Several segments may name one adapter.
+ *   A, B         pools of L adapters, [L, R, K] and [L, N, R], of dtype,
+ *                16-byte aligned
+ *   ranks        DEVICE int32 [L]: adapter a uses rows 0 .. ranks[a] - 1 of A
+ *                and as many columns of B; what lies behind is never used (it
+ *                may hold NaN).  0 <= ranks[a] <= R.
+ *   scales       DEVICE fp32 [L]: s_a
+ * Device-only errors: offsets that descend or leave [0, M], an adapter outside
+ * -1 .. L - 1 or a rank outside 0 .. R set BQ_ERR_UNSUPPORTED in the device
+ * status word; a segment with such offsets is skipped, one with such an
+ * adapter gets no contribution.
+ * Shapes: K, N and R are multiples of 8, 8 <= R <= 128 (other R:
+ * BQ_ERR_UNSUPPORTED), M <= 2^30, K and N <= 2^28; row strides (in elements)
+ * are multiples of 8 and rows 16-byte aligned, so a slice of a fused
+ * projection can be x, base or y.  With BQ_OPT_LINEAR_OVERLAP >= 1 the kernel
+ * takes part in the programmatic dependent launches of bq_linear.
+ *
+ * bq_lora: y[m] = base[m] + s_a (drop(x)[m] A_a^T) B_a^T.
+ *   x        [M, K] of dtype (BQ_BF16 or BQ_F16), row stride ldx
+ *   p, rng   dropout on x, as bq_dropout(x, p, rng) would give it before its
+ *            rounding (p = 0: none, rng may be NULL)
+ *   base     [M, N] of dtype, row stride ldbase; NULL: zeros.  May be y.
+ *   y        [M, N] of dtype, row stride ldy; rows of segments are written in
+ *            full (those without an adapter: base)
+ *   t        NULL, or fp32 [M, R] (16-byte aligned) that receives
+ *            t = drop(x) A_a^T, zero behind the rank, for bq_lora_grad
+ * Products are exact and accumulated in fp32, t enters the second product
+ * with a relative error below 2^-16, y is rounded once.  Deterministic.
+ */
+bq_status bq_lora(const void *x, bq_dtype dtype, int64_t M, int64_t K, int64_t ldx, const void *A, const void *B,
+                  int64_t N, int R, int L, const int32_t *ranks, const float *scales, const int32_t *seg_off,
+                  const int32_t *seg_adapter, int S, double p, const uint64_t *rng, const void *base, int64_t ldbase,
+                  void *y, int64_t ldy, float *t, void *stream);
+
+/*
+ * bq_lora_grad: gradients of bq_lora with respect to x, A and B, from dy.
+ *     dt[m] = s_a dy[m] B_a
+ *     dx[m] = base[m] + mask / (1 - p) * (dt[m] A_a)
+ *     dA_a  = sum over the adapter's rows of dt[m]^T drop(x)[m]     [L, R, K]
+ *     dB_a  = sum over the adapter's rows of s_a dy[m]^T t[m]       [L, N, R]
+ *   dy       [M, N] of dtype, row stride lddy
+ *   x, t     the forward's input and the t that it stored (x is read for dA
+ *            only, t for dB only); p, rng the forward's, unchanged
+ *   base     [M, K] of dtype added to dx (bq_linear_grad_input's result), row
+ *            stride ldbase; NULL: zeros.  May be dx.
+ *   dx       [M, K] of dtype, row stride lddx, rows of segments written in
+ *            full; NULL: not wanted
+ *   dt       fp32 [M, R] scratch (16-byte aligned), needed for dx and dA; it
+ *            holds dt afterwards.  Two calls in flight must not share it.
+ *   dA, dB   fp32, written in full (zero behind the rank and for adapters
+ *            without rows); NULL: not wanted
+ * Segments, adapters, shapes and errors as above.  Sums over rows are fp32 in
+ * a fixed order (deterministic, no atomics).
+ */
+bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int64_t lddy, const void *x, int64_t K,
+                       int64_t ldx, const float *t, const void *A, const void *B, int R, int L, const int32_t *ranks,
+                       const float *scales, const int32_t *seg_off, const int32_t *seg_adapter, int S, double p,
+                       const uint64_t *rng, const void *base, int64_t ldbase, void *dx, int64_t lddx, float *dt,
+                       float *dA, float *dB, void *stream);
+
+/*
  * Options.
  *
  * BQ_OPT_LINEAR_OVERLAP (process-wide, default 0 or the value of the

@@ -35,7 +35,7 @@ EXPORTS = (
     "bq_quantize_mixed",
     "bq_dequantize", "bq_fake_quantize", "bq_linear", "bq_linear_grad_input", "bq_check_division",
     "bq_check_const_division", "bq_quantize_f16s", "bq_linear_f16s", "bq_linear_workspace_bytes", "bq_linear_ws",
-    "bq_selftest_bounded_wait", "bq_set_option", "bq_get_option", "bq_device_status",
+    "bq_dropout", "bq_lora", "bq_lora_grad", "bq_selftest_bounded_wait", "bq_set_option", "bq_get_option", "bq_device_status",
     "bq_status_string", "bq_version",
 )
 BQ_OPT_LINEAR_OVERLAP = 0
@@ -89,6 +89,15 @@ def lib(path: str | None = None):
     L.bq_linear_ws.restype = i32
     L.bq_linear_grad_input.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, i32, i32, i64, i32, vp, vp]
     L.bq_linear_grad_input.restype = i32
+    f64 = ctypes.c_double
+    L.bq_dropout.argtypes = [vp, i32, i64, i64, i64, f64, vp, vp, i64, vp]
+    L.bq_dropout.restype = i32
+    L.bq_lora.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, i32, vp, vp, vp, vp, i32, f64, vp, vp, i64, vp,
+                          i64, vp, vp]
+    L.bq_lora.restype = i32
+    L.bq_lora_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, f64,
+                               vp, vp, i64, vp, i64, vp, vp, vp, vp]
+    L.bq_lora_grad.restype = i32
     L.bq_check_division.argtypes = [ctypes.c_uint32, ctypes.c_uint32, i32, vp, vp]
     L.bq_check_division.restype = i32
     L.bq_check_const_division.argtypes = [i32, ctypes.c_uint32, ctypes.c_uint32, vp, vp]
@@ -263,6 +272,148 @@ def bq_linear_grad_input(dy: torch.Tensor, packed, scales, zeros, K: int, bits: 
                                     _ptr(bit_map_dev), bits, group, K, LAYOUTS[layout], _ptr(dx), _stream(stream))
     _check("bq_linear_grad_input", st)
     return dx
+
+
+# ---------------------------------------------------------------------------
+# dropout and low-rank adapters
+# ---------------------------------------------------------------------------
+
+def _rows_ok(name, v, cols, dtype, device):
+    """v [M, cols] of dtype on device with unit column stride."""
+    if v.dim() != 2 or v.shape[1] != cols or v.dtype != dtype or v.device != device:
+        raise ValueError(f"{name}: [*, {cols}] {dtype} on {device} expected, got {tuple(v.shape)} {v.dtype} on {v.device}")
+    if cols > 1 and v.numel() and v.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+
+
+def _dense(name, v, shape, dtype, device):
+    if tuple(v.shape) != shape or v.dtype != dtype or v.device != device or not v.is_contiguous():
+        raise ValueError(f"{name}: contiguous {shape} {dtype} on {device} expected, got {tuple(v.shape)} {v.dtype} "
+                         f"on {v.device}")
+
+
+def _rng_ptr(rng, device):
+    if rng is None:
+        return None
+    _dense("rng", rng, (2,), torch.int64, device)
+    return rng.data_ptr()
+
+
+def _launch(fn, name, device, stream, *args):
+    """Call `fn` on the tensors' device and its current stream (or `stream`)."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: CUDA tensors expected")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream()
+            st = fn(*args, s.cuda_stream)
+    else:
+        st = fn(*args, stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+    _check(name, st)
+
+
+def bq_dropout(x: torch.Tensor, p: float, rng=None, out=None, stream=None):
+    """mask * x / (1 - p) for x [rows, cols] (fp16 / bf16 / fp32, row stride free), the mask drawn
+    from rng (int64 {seed, offset} on the device) and never stored.  The gradient is the same call on dy."""
+    rows, cols = x.shape
+    _rows_ok("x", x, cols, x.dtype, x.device)
+    o = out if out is not None else torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    _rows_ok("out", o, cols, x.dtype, x.device)
+    if o.shape[0] != rows:
+        raise ValueError("out: as many rows as x expected")
+    _launch(lib().bq_dropout, "bq_dropout", x.device, stream, x.data_ptr(), DTYPE_CODE[x.dtype], rows, cols,
+            x.stride(0), p, _rng_ptr(rng, x.device), o.data_ptr(), o.stride(0))
+    return o
+
+
+def _adapters_ok(A, B, ranks, scales, seg_off, seg_adapter, K, N, dtype, device):
+    L, R = A.shape[0], A.shape[1]
+    S = seg_adapter.shape[0]
+    _dense("A", A, (L, R, K), dtype, device)
+    _dense("B", B, (L, N, R), dtype, device)
+    _dense("ranks", ranks, (L,), torch.int32, device)
+    _dense("scales", scales, (L,), torch.float32, device)
+    _dense("seg_off", seg_off, (S + 1,), torch.int32, device)
+    _dense("seg_adapter", seg_adapter, (S,), torch.int32, device)
+    return L, R, S
+
+
+def bq_lora(x: torch.Tensor, A, B, ranks, scales, seg_off, seg_adapter, base=None, out=None, p: float = 0.0, rng=None,
+            t=None, stream=None):
+    """y [M, N] = base + scales[a] (drop(x) A[a]^T) B[a]^T for the rows of each segment.
+
+    x [M, K] and the pools A [L, R, K], B [L, N, R] in bf16 or fp16; segment i is rows
+    seg_off[i] .. seg_off[i + 1] - 1 with adapter seg_adapter[i] (-1: none); rows behind the last segment keep what
+    `out` holds.  base None: zeros; out may be base (in place) and is allocated when None.  t: fp32 [M, R] that
+    receives drop(x) A[a]^T for bq_lora_grad."""
+    M, K = x.shape
+    N, dtype, dev = B.shape[1], x.dtype, x.device
+    _rows_ok("x", x, K, dtype, dev)
+    L, R, S = _adapters_ok(A, B, ranks, scales, seg_off, seg_adapter, K, N, dtype, dev)
+    y = out
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+    for name, v in (("base", base), ("out", y)):
+        if v is not None:
+            _rows_ok(name, v, N, dtype, dev)
+            if v.shape[0] != M:
+                raise ValueError(f"{name}: {M} rows expected")
+    if t is not None:
+        _dense("t", t, (M, R), torch.float32, dev)
+    _launch(lib().bq_lora, "bq_lora", dev, stream, x.data_ptr(), DTYPE_CODE[dtype], M, K, x.stride(0), A.data_ptr(),
+            B.data_ptr(), N, R, L, ranks.data_ptr(), scales.data_ptr(), seg_off.data_ptr(), seg_adapter.data_ptr(), S, p,
+            _rng_ptr(rng, dev), base.data_ptr() if base is not None else None,
+            base.stride(0) if base is not None else 0, y.data_ptr(), y.stride(0),
+            t.data_ptr() if t is not None else None)
+    return y
+
+
+def bq_lora_grad(dy: torch.Tensor, x, t, A, B, ranks, scales, seg_off, seg_adapter, base=None, out=None,
+                 p: float = 0.0, rng=None, dA=None, dB=None, workspace=None, need_dx: bool = True,
+                 need_weights: bool = True, stream=None):
+    """(dx, dA, dB) of bq_lora from dy [M, N], its input x, the t that it stored and the same p and rng.
+
+    dx = base + mask / (1 - p) (scales[a] (dy B[a]) A[a]) in dy's dtype (base None: zeros; out may be base); dA [L, R, K]
+    and dB [L, N, R] in fp32, written in full.  need_dx / need_weights False skip them (None is returned).
+    workspace: fp32 [M, R] scratch, allocated when None."""
+    M, N = dy.shape
+    L, R, K = A.shape
+    dtype, dev = dy.dtype, dy.device
+    _rows_ok("dy", dy, N, dtype, dev)
+    L, R, S = _adapters_ok(A, B, ranks, scales, seg_off, seg_adapter, K, N, dtype, dev)
+    if need_weights:
+        _rows_ok("x", x, K, dtype, dev)
+        _dense("t", t, (M, R), torch.float32, dev)
+        if x.shape[0] != M:
+            raise ValueError(f"x: {M} rows expected")
+    # what is allocated here belongs to the stream that the kernels run on
+    with torch.cuda.stream(stream):
+        dx = None
+        if need_dx:
+            dx = out if out is not None else torch.empty((M, K), dtype=dtype, device=dev)
+            for name, v in (("base", base), ("out", dx)):
+                if v is not None:
+                    _rows_ok(name, v, K, dtype, dev)
+                    if v.shape[0] != M:
+                        raise ValueError(f"{name}: {M} rows expected")
+        if need_weights:
+            dA = dA if dA is not None else torch.empty((L, R, K), dtype=torch.float32, device=dev)
+            dB = dB if dB is not None else torch.empty((L, N, R), dtype=torch.float32, device=dev)
+            _dense("dA", dA, (L, R, K), torch.float32, dev)
+            _dense("dB", dB, (L, N, R), torch.float32, dev)
+        else:
+            dA = dB = None
+        ws = workspace if workspace is not None else torch.empty((M, R), dtype=torch.float32, device=dev)
+        _dense("workspace", ws, (M, R), torch.float32, dev)
+    ptr = lambda v: v.data_ptr() if v is not None else None  # noqa: E731
+    ld = lambda v: v.stride(0) if v is not None else 0  # noqa: E731
+    xx = x if need_weights else None
+    bb = base if need_dx else None
+    _launch(lib().bq_lora_grad, "bq_lora_grad", dev, stream, dy.data_ptr(), DTYPE_CODE[dtype], M, N, dy.stride(0),
+            ptr(xx), K, ld(xx), ptr(t if need_weights else None), A.data_ptr(), B.data_ptr(), R, L, ranks.data_ptr(),
+            scales.data_ptr(), seg_off.data_ptr(), seg_adapter.data_ptr(), S, p, _rng_ptr(rng, dev), ptr(bb), ld(bb),
+            ptr(dx), ld(dx), ws.data_ptr(), ptr(dA), ptr(dB))
+    return dx, dA, dB
 
 
 def bq_check_division(s_bits_begin: int, s_bits_end: int, refinements: int = 2, stream=None):

@@ -5,6 +5,9 @@ launches, then a device-status check.
     python -m quantized_gemm_group_b200.cases gemm  M N K BITS    # prefill linear, M >= 64
     python -m quantized_gemm_group_b200.cases quant N K BITS      # quantizer, interleaved layout
     python -m quantized_gemm_group_b200.cases grad  M N K BITS    # input gradient dx = dy . dequant(W)
+    python -m quantized_gemm_group_b200.cases lora  M N K R S     # low-rank adapters, S segments, one adapter each
+    python -m quantized_gemm_group_b200.cases lora_grad M N K R S # their gradients
+    python -m quantized_gemm_group_b200.cases dropout M K         # dropout of bf16 activations
 
 Weights are synthetic fp16 N(0, 0.02) (N(0, 0.015) for the prefill case),
 activations (and dy) bf16 N(0, 1); INT4 uses group 128, INT2 group 64.  Each case runs
@@ -47,6 +50,26 @@ def main(argv):
         out = bq.bq_quantize(W, bits, g, "interleaved")
         for _ in range(3):
             bq.bq_quantize(W, bits, g, "interleaved", out=out)
+    elif which in ("lora", "lora_grad"):
+        M, N, K, R, S = (int(v) for v in argv[1:6])
+        x, dy = synth.activations(M, K, seed=2, device="cuda"), synth.activations(M, N, seed=3, device="cuda")
+        ad = synth.adapters(S, R, K, N, seed=4, device="cuda")
+        segs = (torch.linspace(0, M, S + 1, device="cuda").to(torch.int32),
+                torch.arange(S, dtype=torch.int32, device="cuda"))
+        y, dx = torch.empty_like(dy), torch.empty_like(x)
+        t = torch.empty((M, R), dtype=torch.float32, device="cuda")
+        bq.bq_lora(x, *ad, *segs, base=dy, out=y, t=t)
+        for _ in range(3):
+            if which == "lora":
+                bq.bq_lora(x, *ad, *segs, base=dy, out=y)
+            else:
+                bq.bq_lora_grad(dy, x, t, *ad, *segs, base=x, out=dx)
+    elif which == "dropout":
+        M, K = (int(v) for v in argv[1:3])
+        x = synth.activations(M, K, seed=2, device="cuda")
+        rng = torch.tensor([7, 1], dtype=torch.int64, device="cuda")
+        for _ in range(4):
+            bq.bq_dropout(x, 0.05, rng)
     else:
         raise SystemExit(__doc__)
     torch.cuda.synchronize()

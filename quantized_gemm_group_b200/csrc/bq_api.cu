@@ -10,10 +10,12 @@
 #include "../../include/bq.h"
 #include "common.cuh"
 #include "dequant.cuh"
+#include "dropout.cuh"
 #include "fakequant.cuh"
 #include "grad.cuh"
 #include "gemm.cuh"
 #include "gemv.cuh"
+#include "lora.cuh"
 #include "quantize.cuh"
 #include "selftest.cuh"
 
@@ -852,6 +854,264 @@ bq_status linear_any(const void *x, bq_dtype xtype, int64_t M, int64_t K, const 
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------------------
+// dropout and low-rank adapters
+// ---------------------------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxRows = 1ll << 30, kMaxCols = 1ll << 28;
+
+// thr = round(p 65536); false where p is no probability below 1 - 2^-17.
+bool drop_args(double p, const uint64_t *rng, DropArgs *d) {
+  if (!(p >= 0.0) || !(p < 1.0)) return false;
+  const uint32_t thr = (uint32_t)(p * 65536.0 + 0.5);
+  if (thr > 65535) return false;
+  d->thr = thr;
+  d->inv_keep = (float)(65536.0 / (65536.0 - (double)thr));
+  d->rng = reinterpret_cast<const unsigned long long *>(rng);
+  return true;
+}
+
+template <int DT>
+bq_status launch_dropout(const void *x, int64_t rows, int64_t cols, int64_t ldx, void *out, int64_t ldo,
+                         const DropArgs &d, cudaStream_t st) {
+  using T = typename DropElem<DT>::T;
+  const int64_t total = rows * ((cols + 7) / 8);
+  int64_t grid = (total + kThreads - 1) / kThreads;
+  const int64_t cap = (int64_t)sm_count() * 8;
+  if (grid > cap) grid = cap;
+  const bool vec = aligned(x, 16) && aligned(out, 16) && (rows == 1 || ((ldx * sizeof(T)) % 16 == 0 && (ldo * sizeof(T)) % 16 == 0));
+  const T *xi = reinterpret_cast<const T *>(x);
+  T *o = reinterpret_cast<T *>(out);
+  if (vec) dropout_kernel<DT, true><<<grid, kThreads, 0, st>>>(xi, rows, cols, ldx, o, ldo, d);
+  else dropout_kernel<DT, false><<<grid, kThreads, 0, st>>>(xi, rows, cols, ldx, o, ldo, d);
+  return launch_status();
+}
+
+// Launch with clusters of cs CTAs along x; overlap: programmatic dependent launch.
+template <typename Kern, typename Args>
+bq_status launch_cluster(Kern kern, int64_t grid, int cs, int smem, bool overlap, const Args &a, cudaStream_t st) {
+  if (grid > 0x7fffffffll) return BQ_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kLoraThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = (unsigned)cs;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = overlap ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+    cudaGetLastError();
+    return BQ_ERR_CUDA;
+  }
+  return BQ_OK;
+}
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+template <int XT, int UP, int BM, int RP>
+bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
+  using G = LoraGeom<BM, RP>;
+  const int64_t cut = a.M / BM + a.S, tiles = cut < a.M ? cut : a.M;
+  // CTAs per tile: as many as keep the grid within a few waves
+  int cs = 8;
+  while (cs > 1 && tiles * cs > 6 * (int64_t)sm_count()) cs /= 2;
+  a.CS = cs;
+  a.slice_c = (int)round_up((a.Ci + cs - 1) / cs, G::SC);
+  a.slice_o = (int)round_up((a.Co + cs - 1) / cs, 32);
+  constexpr auto kern = lora_kernel<XT, UP, BM, RP>;
+  if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
+  return launch_cluster(kern, tiles * cs, cs, G::TOTAL, overlap_mode() >= 1, a, st);
+}
+
+template <int XT, int UP>
+bq_status launch_lora(const LoraArgs &a, cudaStream_t st) {
+  if (a.M == 0 || a.S == 0) return BQ_OK;
+  const bool small = a.M <= 24 * (int64_t)a.S;  // few rows a segment: 16-row tiles
+  if (a.R <= 16) return small ? launch_lora_t<XT, UP, 16, 16>(a, st) : launch_lora_t<XT, UP, 64, 16>(a, st);
+  if (a.R <= 64) return small ? launch_lora_t<XT, UP, 16, 64>(a, st) : launch_lora_t<XT, UP, 64, 64>(a, st);
+  return small ? launch_lora_t<XT, UP, 16, 128>(a, st) : launch_lora_t<XT, UP, 64, 128>(a, st);
+}
+
+template <int XT, int RP>
+bq_status launch_wgrad_t(LoraWgradArgs a, cudaStream_t st) {
+  using G = WgradGeom<RP>;
+  if (a.dA.out) a.dA.tiles = (a.dA.C + G::CT - 1) / G::CT;
+  if (a.dB.out) a.dB.tiles = (a.dB.C + G::CT - 1) / G::CT;
+  const int64_t clusters = (int64_t)a.L * (a.dA.tiles + a.dB.tiles);
+  if (clusters == 0) return BQ_OK;
+  a.CS = 8;
+  constexpr auto kern = lora_wgrad_kernel<XT, RP>;
+  if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
+  return launch_cluster(kern, clusters * a.CS, a.CS, G::TOTAL, false, a, st);
+}
+
+template <int XT>
+bq_status launch_wgrad(const LoraWgradArgs &a, cudaStream_t st) {
+  if (a.R <= 16) return launch_wgrad_t<XT, 16>(a, st);
+  if (a.R <= 64) return launch_wgrad_t<XT, 64>(a, st);
+  return launch_wgrad_t<XT, 128>(a, st);
+}
+
+// What bq_lora and bq_lora_grad have in common.
+bq_status lora_check(bq_dtype dtype, int64_t M, int64_t K, int64_t N, int R, int L, int S) {
+  if (M < 0 || K < 0 || N < 0 || R < 0 || L < 0 || S < 0) return BQ_ERR_SHAPE;
+  if (dtype != BQ_F16 && dtype != BQ_BF16) return BQ_ERR_UNSUPPORTED;
+  if (R > 128 || R == 0) return BQ_ERR_UNSUPPORTED;
+  if (R % 8 || K % 8 || N % 8 || M > kMaxRows || K > kMaxCols || N > kMaxCols) return BQ_ERR_SHAPE;
+  return BQ_OK;
+}
+
+// A [rows, cols] 16-bit operand with 16-byte aligned rows.
+bq_status lora_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld) {
+  if (rows == 0 || cols == 0) return BQ_OK;
+  if (!p) return BQ_ERR_NULL;
+  if (rows > 1 && (ld < cols || ld % 8)) return BQ_ERR_SHAPE;
+  return aligned(p, 16) ? BQ_OK : BQ_ERR_ALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+bq_status bq_dropout(const void *x, bq_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, double p,
+                     const uint64_t *rng, void *out, int64_t ldo, void *stream) {
+  if (rows < 0 || cols < 0 || rows > (1ll << 32) || cols > (1ll << 34)) return BQ_ERR_SHAPE;
+  if (dtype != BQ_F16 && dtype != BQ_BF16 && dtype != BQ_F32) return BQ_ERR_UNSUPPORTED;
+  DropArgs d = {};
+  if (!drop_args(p, rng, &d)) return BQ_ERR_UNSUPPORTED;
+  if (rows > 1 && (ldx < cols || ldo < cols)) return BQ_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return BQ_OK;
+  if (!x || !out || (d.thr && !rng)) return BQ_ERR_NULL;
+  const size_t es = dtype == BQ_F32 ? 4 : 2;
+  if (!aligned(x, es) || !aligned(out, es) || (d.thr && !aligned(rng, 8))) return BQ_ERR_ALIGN;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == BQ_F32) return launch_dropout<2>(x, rows, cols, ldx, out, ldo, d, st);
+  if (dtype == BQ_BF16) return launch_dropout<1>(x, rows, cols, ldx, out, ldo, d, st);
+  return launch_dropout<0>(x, rows, cols, ldx, out, ldo, d, st);
+}
+
+bq_status bq_lora(const void *x, bq_dtype dtype, int64_t M, int64_t K, int64_t ldx, const void *A, const void *B,
+                  int64_t N, int R, int L, const int32_t *ranks, const float *scales, const int32_t *seg_off,
+                  const int32_t *seg_adapter, int S, double p, const uint64_t *rng, const void *base, int64_t ldbase,
+                  void *y, int64_t ldy, float *t, void *stream) {
+  bq_status s = lora_check(dtype, M, K, N, R, L, S);
+  if (s != BQ_OK) return s;
+  LoraArgs a = {};
+  if (!drop_args(p, rng, &a.drop)) return BQ_ERR_UNSUPPORTED;
+  if (M == 0 || S == 0) return BQ_OK;
+  if ((s = lora_matrix(x, M, K, ldx)) != BQ_OK) return s;
+  if ((s = lora_matrix(y, M, N, ldy)) != BQ_OK) return s;
+  if (base && (s = lora_matrix(base, M, N, ldbase)) != BQ_OK) return s;
+  if ((s = lora_matrix(A, L, K, K)) != BQ_OK || (s = lora_matrix(B, L, N, N)) != BQ_OK) return s;
+  if (!seg_off || !seg_adapter || (L && (!ranks || !scales)) || (a.drop.thr && !rng)) return BQ_ERR_NULL;
+  if (!aligned(seg_off, 4) || !aligned(seg_adapter, 4) || !aligned(ranks, 4) || !aligned(scales, 4) ||
+      !aligned(t, 16) || (a.drop.thr && !aligned(rng, 8)))
+    return BQ_ERR_ALIGN;
+  a.x = reinterpret_cast<const uint16_t *>(x);
+  a.A = reinterpret_cast<const uint16_t *>(A);
+  a.B = reinterpret_cast<const uint16_t *>(B);
+  a.base = reinterpret_cast<const uint16_t *>(base);
+  a.y = reinterpret_cast<uint16_t *>(y);
+  a.t = t;
+  a.ranks = ranks;
+  a.scales = scales;
+  a.seg_off = seg_off;
+  a.seg_adapter = seg_adapter;
+  a.M = M;
+  a.ldx = ldx;
+  a.ldbase = ldbase;
+  a.ldy = ldy;
+  a.Ci = (int)K;
+  a.Co = (int)N;
+  a.R = R;
+  a.L = L;
+  a.S = S;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == BQ_BF16 ? launch_lora<1, 0>(a, st) : launch_lora<0, 0>(a, st);
+}
+
+bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int64_t lddy, const void *x, int64_t K,
+                       int64_t ldx, const float *t, const void *A, const void *B, int R, int L, const int32_t *ranks,
+                       const float *scales, const int32_t *seg_off, const int32_t *seg_adapter, int S, double p,
+                       const uint64_t *rng, const void *base, int64_t ldbase, void *dx, int64_t lddx, float *dt,
+                       float *dA, float *dB, void *stream) {
+  bq_status s = lora_check(dtype, M, K, N, R, L, S);
+  if (s != BQ_OK) return s;
+  LoraArgs a = {};
+  if (!drop_args(p, rng, &a.drop)) return BQ_ERR_UNSUPPORTED;
+  const bool rows = M > 0 && S > 0;
+  const bool need_dt = dx || dA;
+  if (rows) {
+    if ((s = lora_matrix(dy, M, N, lddy)) != BQ_OK) return s;
+    if (dA && (s = lora_matrix(x, M, K, ldx)) != BQ_OK) return s;
+    if (dx && (s = lora_matrix(dx, M, K, lddx)) != BQ_OK) return s;
+    if (dx && base && (s = lora_matrix(base, M, K, ldbase)) != BQ_OK) return s;
+    if (dx && (s = lora_matrix(A, L, K, K)) != BQ_OK) return s;
+    if (need_dt && (s = lora_matrix(B, L, N, N)) != BQ_OK) return s;
+    if (!seg_off || !seg_adapter || (need_dt && !dt) || (dB && !t) || (a.drop.thr && !rng)) return BQ_ERR_NULL;
+  }
+  if (L && (!ranks || !scales)) return BQ_ERR_NULL;
+  if (!aligned(seg_off, 4) || !aligned(seg_adapter, 4) || !aligned(ranks, 4) || !aligned(scales, 4) ||
+      !aligned(t, 16) || !aligned(dt, 16) || !aligned(dA, 16) || !aligned(dB, 16) ||
+      (a.drop.thr && !aligned(rng, 8)))
+    return BQ_ERR_ALIGN;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (rows && need_dt) {
+    a.x = reinterpret_cast<const uint16_t *>(dy);
+    a.A = reinterpret_cast<const uint16_t *>(A);
+    a.B = reinterpret_cast<const uint16_t *>(B);
+    a.base = reinterpret_cast<const uint16_t *>(dx ? base : nullptr);
+    a.y = reinterpret_cast<uint16_t *>(dx);
+    a.t = dt;
+    a.ranks = ranks;
+    a.scales = scales;
+    a.seg_off = seg_off;
+    a.seg_adapter = seg_adapter;
+    a.M = M;
+    a.ldx = lddy;
+    a.ldbase = ldbase;
+    a.ldy = lddx;
+    a.Ci = (int)N;
+    a.Co = dx ? (int)K : 0;
+    a.R = R;
+    a.L = L;
+    a.S = S;
+    s = dtype == BQ_BF16 ? launch_lora<1, 1>(a, st) : launch_lora<0, 1>(a, st);
+    if (s != BQ_OK) return s;
+  }
+  LoraWgradArgs w = {};
+  w.dA.X = reinterpret_cast<const uint16_t *>(x);
+  w.dA.P = dt;
+  w.dA.out = dA;
+  w.dA.ldx = ldx;
+  w.dA.C = (int)K;
+  w.dB.X = reinterpret_cast<const uint16_t *>(dy);
+  w.dB.P = t;
+  w.dB.out = dB;
+  w.dB.ldx = lddy;
+  w.dB.C = (int)N;
+  w.ranks = ranks;
+  w.scales = scales;
+  w.seg_off = seg_off;
+  w.seg_adapter = seg_adapter;
+  w.M = M;
+  w.R = R;
+  w.L = L;
+  w.S = rows ? S : 0;
+  w.drop = a.drop;
+  return dtype == BQ_BF16 ? launch_wgrad<1>(w, st) : launch_wgrad<0>(w, st);
+}
+
+}  // extern "C"
 
 extern "C" {
 

@@ -1,0 +1,940 @@
+// lora.cuh -- low-rank adapters beside a shared projection: for each row m of
+// a segment with adapter a (rank r_a <= R, scale s_a)
+//   forward         t = drop(x) A^T          y  = base + s (t B^T)
+//   input gradient  dt = s (dy B)            dx = base + drop'(dt A)
+// Both directions are one shape of work, "down" to the rank and "up" again,
+// so one kernel does both (UP = 0 forward, 1 gradient); they differ in which
+// pool comes first and in how its elements lie: A is [L, R, K] (contiguous
+// along the contraction of the forward's down step), B is [L, N, R].
+//
+// Bound: memory.  x and base are read once and y written once; with r <= 64
+// the products cost less than the traffic on mma.sync, so that the tensor
+// memory path would gain nothing here.
+//
+// Split: a cluster of CS CTAs owns a tile of BM rows of one segment.  Each CTA
+// contracts its share of the columns (down), the partial [BM, R] sums meet in
+// distributed shared memory (added in rank order: no atomics, the same bits
+// every time), and each CTA then writes its share of the output columns (up).
+// t never goes through global memory (the training forward stores it once for
+// the backward pass), and one launch does the whole adapter.  The grid has
+// one cluster for each tile that S segments of M rows can need; a cluster
+// finds its segment by a prefix sum over the segment lengths, so lengths stay
+// on the device.
+//
+// Down: a warp takes 16 MT rows and every KQ-th run of 32 columns.  A lane's
+// 16-byte load of a row (8 consecutive columns) is used as the fragments of
+// two k-steps: the contraction may run in any order as long as both operands
+// use the same one, so x needs no shared memory and dropout is applied to the
+// loaded registers, one generator block a load.  The pool goes through a
+// cp.async ring shared by the row groups.
+// Up: t (fp32) is split into two bf16 parts t = hi + lo (relative error below
+// 2^-17; one bf16 would lose 2^-9 of it), two mma.sync a step.  fp16
+// pools are split into two bf16 parts as well (11 bits = 8 + 3, exact): t does
+// not have fp16's range.  A warp takes 32 output columns of the tile; the
+// column that fragment slot n of tile j stands for is 8 (n / 2) + 2 j + n % 2,
+// so that a lane ends with 8 consecutive columns: base and y move as 16-byte
+// vectors straight from and to registers.
+#pragma once
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "dropout.cuh"
+#include "gemv.cuh"
+
+namespace bq {
+namespace cg = cooperative_groups;
+
+constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+
+struct LoraArgs {
+  const uint16_t *x;      // [M, Ci] rows of stride ldx: x, or dy
+  const uint16_t *A, *B;  // pools [L, R, K] and [L, N, R]
+  const uint16_t *base;   // [M, Co] added to the output, or NULL
+  uint16_t *y;            // [M, Co]; may be base
+  float *t;               // [M, R] or NULL: t (UP = 0), dt (UP = 1)
+  const int *ranks;
+  const float *scales;
+  const int *seg_off, *seg_adapter;
+  int64_t M, ldx, ldbase, ldy;
+  int Ci, Co, R, L, S, CS;
+  int slice_c, slice_o;  // columns of the contraction / of the output per CTA
+  DropArgs drop;
+};
+
+// One segment tile: rows [row0, row0 + rows), its adapter (-1: none).
+struct LoraTile {
+  int row0, rows, adapter;
+  bool found;
+};
+
+// A segment as the kernels use it: its length, 0 where the offsets are unusable.
+BQ_DEV int lora_segment(const int *seg_off, int s, int64_t M, int *start) {
+  const int a = seg_off[s], b = seg_off[s + 1];
+  *start = a;
+  return (a >= 0 && b >= a && b <= M) ? b - a : 0;
+}
+
+// Tile `tile` of the segments cut into BM rows each.  Every lane of the warp
+// takes part; the result is the same in all lanes.
+template <int BM>
+BQ_DEV LoraTile lora_find_tile(const int *seg_off, const int *seg_adapter, int S, int64_t M, int tile) {
+  const int lane = threadIdx.x & 31;
+  LoraTile r = {0, 0, -1, false};
+  int before = 0;
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int s = s0 + lane;
+    int start = 0, len = 0, ad = -1;
+    if (s < S) {
+      ad = seg_adapter[s];
+      len = lora_segment(seg_off, s, M, &start);
+    }
+    const int n = (len + BM - 1) / BM;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > tile);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int i = tile - before - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, n, src));
+      const int st = __shfl_sync(0xffffffffu, start, src), ln = __shfl_sync(0xffffffffu, len, src);
+      r.row0 = st + i * BM;
+      r.rows = min(BM, ln - i * BM);
+      r.adapter = __shfl_sync(0xffffffffu, ad, src);
+      r.found = true;
+      return r;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
+// Descending or overlong segments and unknown adapters or ranks are recorded
+// in the device status (one warp of the grid looks at all of them).
+BQ_DEV void lora_check_segments(const int *seg_off, const int *seg_adapter, const int *ranks, int S, int L, int R,
+                                int64_t M) {
+  bool bad = false;
+  for (int s = threadIdx.x & 31; s < S; s += 32) {
+    const int a = seg_off[s], b = seg_off[s + 1], ad = seg_adapter[s];
+    bad |= a < 0 || b < a || b > M || ad < -1 || ad >= L;
+    if (ad >= 0 && ad < L) bad |= ranks[ad] < 0 || ranks[ad] > R;
+  }
+  if (bad) bq_flag(BQ_FLAG_BADMAP);
+}
+
+// The rank to use: 0 (no contribution) without an adapter or with a bad one.
+BQ_DEV int lora_rank(const int *ranks, int adapter, int L, int R) {
+  if (adapter < 0 || adapter >= L) return 0;
+  const int r = ranks[adapter];
+  return (r < 0 || r > R) ? 0 : r;
+}
+
+BQ_DEV void cp_async16(uint32_t dst, const void *src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+BQ_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> BQ_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+BQ_DEV void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t smem_addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_addr));
+}
+BQ_DEV uint2 lds_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+BQ_DEV void sts_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+BQ_DEV void sts_v2f(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+BQ_DEV uint4 ld_nc_v4(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// Two floats as bf16x2 (a in the lower half).
+BQ_DEV uint32_t pack_bf16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// v = hi + lo in bf16 parts; an infinite or NaN v keeps lo = 0.
+BQ_DEV void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16(a, b);
+  float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+  if (!(fabsf(ra) <= 3.402823466e38f)) ra = 0.0f;
+  if (!(fabsf(rb) <= 3.402823466e38f)) rb = 0.0f;
+  lo = pack_bf16(ra, rb);
+}
+// A 16-bit pair of the pool's type as two bf16x2 parts (bf16: lo unused).
+template <int XT> BQ_DEV void pool_parts(uint32_t w, uint32_t &hi, uint32_t &lo) {
+  if (XT == 1) {
+    hi = w;
+    lo = 0;
+  } else {
+    const float2 f = Elem<0>::pair(w);
+    split_bf16(f.x, f.y, hi, lo);
+  }
+}
+
+// Tile geometry for BM rows and the padded rank RP.
+template <int BM, int RP> struct LoraGeom {
+  static constexpr int MT = (BM == 16 || RP == 128) ? 1 : 2;  // 16-row tiles per warp (down)
+  static constexpr int RG = BM / (16 * MT);                   // row groups
+  static constexpr int KQ = kLoraWarps / RG;                  // warps sharing a step's columns
+  static constexpr int SC = 32 * KQ;                          // columns per step
+  static constexpr int NST = (BM == 16 && RP == 128) ? 2 : 3;
+  static constexpr int STAGE = RP * SC * 2;                   // pool bytes per stage
+  static constexpr int PARTIAL = KQ * BM * RP * 4;            // the warps' partial sums
+  static constexpr int T_BYTES = 2 * BM * RP * 2;             // t as two bf16 parts
+  static constexpr int WT_BYTES = RP * 64;                    // a warp's 32 columns of A (UP = 1)
+  static constexpr int MAIN0 = (NST * STAGE > PARTIAL) ? NST * STAGE : PARTIAL;
+  static constexpr int UPB = T_BYTES + kLoraWarps * WT_BYTES;
+  static constexpr int MAIN = (MAIN0 > UPB) ? MAIN0 : UPB;
+  static constexpr int RECV = BM * RP * 4;
+  static constexpr int TOTAL = MAIN + RECV;
+};
+
+// Shared-memory byte offset of 16-byte chunk c of row r in a stage of the
+// down pool.  UP = 0: row = rank, SC columns; two rows of four chunks are
+// read together.  UP = 1: row = contraction index, RP ranks; the eight rows
+// 8 i + {0, 1} of one transposed fragment are read together.
+template <int UP, int RP, int SC> BQ_DEV uint32_t down_offset(int r, int c) {
+  if (UP == 0) return (uint32_t)(r * SC * 2 + ((c ^ ((r & 1) << 2)) << 4));
+  int f;
+  if (RP >= 64) f = (((r >> 3) & 3) << 1) | (r & 1);
+  else if (RP == 32) f = (r >> 3) & 3;
+  else f = (r >> 3) & 1;
+  return (uint32_t)(r * RP * 2 + ((c ^ f) << 4));
+}
+
+// grid = CS x tiles, cluster = (CS, 1, 1).
+template <int XT, int UP, int BM, int RP>
+__global__ void __launch_bounds__(kLoraThreads, (RP == 128 || (XT == 0 && RP == 64)) ? 1 : 2)
+lora_kernel(LoraArgs a) {
+  using G = LoraGeom<BM, RP>;
+  constexpr int MT = G::MT, RG = G::RG, KQ = G::KQ, SC = G::SC, NST = G::NST;
+  constexpr int NT = RP / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CS = a.CS, rank = (int)blockIdx.x % CS, tile_index = (int)blockIdx.x / CS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const uint32_t sbase = smem_u32(smem);
+
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x == 0 && warp == kLoraWarps - 1)
+    lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
+  const LoraTile tile = lora_find_tile<BM>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
+  if (!tile.found) return;  // the whole cluster
+  const int r_a = lora_rank(a.ranks, tile.adapter, a.L, a.R);
+  const int o_begin = rank * a.slice_o, o_end = min(a.Co, o_begin + a.slice_o);
+
+  if (r_a == 0) {
+    // no contribution: the rows are base's (nothing to do in place), t is zero
+    if (a.base != a.y) {
+      const int per = (o_end - o_begin) / 8;  // 16-byte pieces of a row (may be <= 0)
+      for (int i = threadIdx.x; per > 0 && i < per * tile.rows; i += kLoraThreads) {
+        const int m = i / per, c = o_begin + 8 * (i - m * per);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (a.base) v = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m) * a.ldbase + c);
+        *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + c) = v;
+      }
+    }
+    if (a.t && rank == 0)
+      for (int i = threadIdx.x; i < tile.rows * a.R; i += kLoraThreads) a.t[(int64_t)tile.row0 * a.R + i] = 0.0f;
+    return;
+  }
+  // every CTA has started before any writes into its shared memory
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+  const bool drop = a.drop.thr != 0;
+  const DropState dst = drop_state(a.drop);
+  const int K = UP ? a.Co : a.Ci, N = UP ? a.Ci : a.Co;
+  const uint16_t *poolA = a.A + (int64_t)tile.adapter * a.R * K;  // [R, K]
+  const uint16_t *poolB = a.B + (int64_t)tile.adapter * a.R * N;  // [N, R]
+  const uint16_t *down = UP ? poolB : poolA;
+  const int nt_used = (r_a + 7) / 8;
+
+  // ---- down: partial sums of this warp's rows over its columns -------------
+  const int rg = warp % RG, kq = warp / RG;
+  const int c_begin = rank * a.slice_c, c_end = min(a.Ci, c_begin + a.slice_c);
+  const int steps = (c_end > c_begin) ? (c_end - c_begin + SC - 1) / SC : 0;
+  const uint16_t *xrow[MT][2];
+  bool xval[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = (rg * MT + mt) * 16 + h * 8 + g;
+      xval[mt][h] = m < tile.rows;
+      xrow[mt][h] = a.x + (int64_t)(tile.row0 + (xval[mt][h] ? m : 0)) * a.ldx;
+    }
+  const int lane_c = 32 * kq + 8 * t4;
+  auto load_x = [&](uint4 (&v)[MT][2], int step) {
+    const int c = c_begin + step * SC + lane_c;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[mt][h] = (step < steps && c < c_end && xval[mt][h]) ? ld_stream_v4(xrow[mt][h] + c) : make_uint4(0, 0, 0, 0);
+  };
+  auto load_pool = [&](int step) {
+    if (step < steps) {
+      const uint32_t stage = sbase + (step % NST) * G::STAGE;
+      const int c0 = c_begin + step * SC;
+      if (UP == 0) {
+        constexpr int CH = SC / 8;
+        for (int i = threadIdx.x; i < r_a * CH; i += kLoraThreads) {
+          const int r = i / CH, c = i % CH;
+          const bool ok = c0 + 8 * c < c_end;
+          cp_async16(stage + down_offset<UP, RP, SC>(r, c), down + (int64_t)r * K + (ok ? c0 + 8 * c : 0), ok);
+        }
+      } else {
+        for (int i = threadIdx.x; i < nt_used * SC; i += kLoraThreads) {
+          const int r = i / nt_used, c = i - r * nt_used;
+          const bool ok = c0 + r < c_end;
+          cp_async16(stage + down_offset<UP, RP, SC>(r, c), down + (int64_t)(ok ? c0 + r : 0) * a.R + 8 * c, ok);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.0f;
+
+  uint4 xv[2][MT][2];
+  load_x(xv[0], 0);
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s) load_pool(s);
+  auto run_step = [&](uint4 (&cur)[MT][2], uint4 (&nxt)[MT][2], int step) {
+    load_x(nxt, step + 1);
+    cp_async_wait<NST - 2>();
+    __syncthreads();  // the stage is visible, and the one read last step is free
+    load_pool(step + NST - 1);
+    if (UP == 0 && drop) {
+      const int c = c_begin + step * SC + lane_c;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int m = (rg * MT + mt) * 16 + h * 8 + g;
+          const uint4 k = drop_mask8(drop_block(dst, (uint32_t)c >> 3, (uint32_t)(tile.row0 + m)), dst.thr_hi);
+          cur[mt][h].x &= k.x;
+          cur[mt][h].y &= k.y;
+          cur[mt][h].z &= k.z;
+          cur[mt][h].w &= k.w;
+        }
+    }
+    const uint32_t stage = sbase + (step % NST) * G::STAGE;
+    uint32_t fa[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      fa[mt][0][0] = cur[mt][0].x;
+      fa[mt][0][1] = cur[mt][1].x;
+      fa[mt][0][2] = cur[mt][0].y;
+      fa[mt][0][3] = cur[mt][1].y;
+      fa[mt][1][0] = cur[mt][0].z;
+      fa[mt][1][1] = cur[mt][1].z;
+      fa[mt][1][2] = cur[mt][0].w;
+      fa[mt][1][3] = cur[mt][1].w;
+    }
+    if (UP == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (nt < nt_used) {
+          const uint4 w = lds_v4(stage + down_offset<UP, RP, SC>(nt * 8 + g, 4 * kq + t4));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            MmaT<XT>::mma(acc[mt][nt], fa[mt][0], w.x, w.y);
+            MmaT<XT>::mma(acc[mt][nt], fa[mt][1], w.z, w.w);
+          }
+        }
+    } else {
+      // lane i addresses row i % 8 of matrix i / 8: (nt, low), (nt, high), (nt + 1, low), (nt + 1, high)
+      const int j = lane & 7, hi = (lane >> 3) & 1, nx = lane >> 4;
+      const int row = 32 * kq + 8 * (j >> 1) + (j & 1) + 2 * hi;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt += 2)
+        if (nt < nt_used) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            uint32_t w[4];
+            ldmatrix_x4_trans(w, stage + down_offset<UP, RP, SC>(row + 4 * ks, nt + nx));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              MmaT<XT>::mma(acc[mt][nt], fa[mt][ks], w[0], w[1]);
+              MmaT<XT>::mma(acc[mt][nt + 1], fa[mt][ks], w[2], w[3]);
+            }
+          }
+        }
+    }
+  };
+  for (int step = 0; step < steps; step += 2) {
+    run_step(xv[0], xv[1], step);
+    if (step + 1 < steps) run_step(xv[1], xv[0], step + 1);
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // ---- the sums meet: warps in this CTA's memory, CTAs in their owner's ----
+  float *part = reinterpret_cast<float *>(smem);  // [KQ][BM][RP]
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int m = (rg * MT + mt) * 16 + g;
+      float *p = part + ((kq * BM + m) * RP + nt * 8 + 2 * t4);
+      *reinterpret_cast<float2 *>(p) = make_float2(acc[mt][nt][0], acc[mt][nt][1]);
+      *reinterpret_cast<float2 *>(p + 8 * RP) = make_float2(acc[mt][nt][2], acc[mt][nt][3]);
+    }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  const int per = BM * RP / CS;  // elements that one CTA owns
+  float *recv = reinterpret_cast<float *>(smem + G::MAIN);  // [CS][per]
+  for (int e = 4 * (int)threadIdx.x; e < BM * RP; e += 4 * kLoraThreads) {
+    float4 s = *reinterpret_cast<const float4 *>(part + e);
+#pragma unroll
+    for (int q = 1; q < KQ; ++q) {
+      const float4 v = *reinterpret_cast<const float4 *>(part + q * BM * RP + e);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    const int owner = e / per;
+    *reinterpret_cast<float4 *>(cluster.map_shared_rank(recv, owner) + rank * per + (e - owner * per)) = s;
+  }
+  cluster.sync();
+  {
+    const float sc = a.scales[tile.adapter];
+    const float pre = (UP == 0) ? a.drop.inv_keep : sc;  // to t (or dt) as stored
+    const float post = (UP == 0) ? sc : 1.0f;                          // to what the up step multiplies
+    for (int i = 4 * (int)threadIdx.x; i < per; i += 4 * kLoraThreads) {
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < CS; ++q) {
+        const float4 p = *reinterpret_cast<const float4 *>(recv + q * per + i);
+        v[0] += p.x;
+        v[1] += p.y;
+        v[2] += p.z;
+        v[3] += p.w;
+      }
+      const int e = rank * per + i, m = e / RP, r = e % RP;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = (r + k < r_a) ? v[k] * pre : 0.0f;
+      if (a.t && m < tile.rows && r < a.R)
+        *reinterpret_cast<float4 *>(a.t + (int64_t)(tile.row0 + m) * a.R + r) = make_float4(v[0], v[1], v[2], v[3]);
+      uint2 hi, lo;
+      split_bf16(v[0] * post, v[1] * post, hi.x, lo.x);
+      split_bf16(v[2] * post, v[3] * post, hi.y, lo.y);
+      int c = r >> 3;
+      if (RP >= 64) c ^= (m & 1) << 2;
+      const int at = m * RP * 2 + c * 16 + (r & 7) * 2;
+      for (int q = 0; q < CS; ++q) {
+        uint8_t *tt = cluster.map_shared_rank(smem, q);
+        *reinterpret_cast<uint2 *>(tt + at) = hi;
+        *reinterpret_cast<uint2 *>(tt + BM * RP * 2 + at) = lo;
+      }
+    }
+  }
+  cluster.sync();
+
+  // ---- up: this CTA's output columns, 32 per warp and turn -----------------
+  constexpr int MTU = BM / 16;             // 16-row tiles
+  constexpr int KC = (RP >= 32) ? RP / 32 : 1;  // runs of 32 ranks (one of 16 where RP = 16)
+  constexpr int KS = (RP >= 32) ? 2 : 1;   // k-steps in a run
+  const uint32_t tbase = sbase, wbase = sbase + G::T_BYTES + warp * G::WT_BYTES;
+  const float out_scale = (UP == 1) ? a.drop.inv_keep : 1.0f;
+  for (int cb = o_begin + 32 * warp; cb < o_end; cb += 32 * kLoraWarps) {
+    uint32_t w[4][KC][KS][2];  // fragments of the up pool: n-tile, run, k-step
+    if (UP == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = cb + 8 * (g >> 1) + 2 * j + (g & 1);
+        const uint16_t *p = poolB + (int64_t)n * a.R;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+          constexpr int PER = 4 * KS;  // ranks that a lane holds of a run
+          const int r = 32 * i + PER * t4, left = r_a - r;
+          uint32_t v[4] = {0, 0, 0, 0};
+          if (n < o_end && left > 0) {
+            if (KS == 2) {
+              const uint4 q = ld_nc_v4(p + r);
+              v[0] = q.x;
+              v[1] = q.y;
+              v[2] = q.z;
+              v[3] = q.w;
+            } else {
+              const uint2 q = *reinterpret_cast<const uint2 *>(p + r);
+              v[0] = q.x;
+              v[1] = q.y;
+            }
+            if (left < PER)  // what lies behind the rank may be anything
+#pragma unroll
+              for (int k = 0; k < PER / 2; ++k)
+                v[k] &= (left > 2 * k + 1) ? 0xffffffffu : (left > 2 * k) ? 0x0000ffffu : 0u;
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            w[j][i][ks][0] = v[2 * ks];
+            w[j][i][ks][1] = v[2 * ks + 1];
+          }
+        }
+      }
+    } else {
+      // 32 columns of A [R, K], stored so that a transposed read gives the
+      // column order above: pair p = 4 q + j of a row goes to tile j, place q
+      __syncwarp();
+      const int rows = (RP >= 32) ? (r_a + 31) & ~31 : 16;
+      for (int i = lane; i < rows * 4; i += 32) {
+        const int q = i & 3;
+        // the eight rows of one store instruction lie in different banks
+        const int i8 = (i >> 2) & 7, blk = i >> 5;
+        int r;
+        if (RP >= 32) {
+          r = 32 * (blk >> 2) + 8 * (i8 >> 1) + 2 * (blk & 3) + (i8 & 1);
+        } else {
+          r = 4 * (i8 >> 1) + 2 * blk + (i8 & 1);
+        }
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < r_a && cb + 8 * q < o_end) v = ld_nc_v4(poolA + (int64_t)r * K + cb + 8 * q);
+        const int f = (RP >= 32) ? (r >> 3) & 3 : (r >> 2) & 3;
+        const uint32_t at = wbase + r * 64 + q * 4;
+        sts_u32(at + ((0 ^ f) << 4), v.x);
+        sts_u32(at + ((1 ^ f) << 4), v.y);
+        sts_u32(at + ((2 ^ f) << 4), v.z);
+        sts_u32(at + ((3 ^ f) << 4), v.w);
+      }
+      __syncwarp();
+      const int l = lane & 7, hi = (lane >> 3) & 1, jx = lane >> 4;
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int r = (RP >= 32) ? 32 * i + 8 * (l >> 1) + 4 * ks + (l & 1) + 2 * hi : 4 * (l >> 1) + (l & 1) + 2 * hi;
+          const int f = (RP >= 32) ? (r >> 3) & 3 : (r >> 2) & 3;
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            uint32_t q[4] = {0, 0, 0, 0};
+            if (32 * i < r_a) ldmatrix_x4_trans(q, wbase + r * 64 + (((j + jx) ^ f) << 4));
+            w[j][i][ks][0] = q[0];
+            w[j][i][ks][1] = q[1];
+            w[j + 1][i][ks][0] = q[2];
+            w[j + 1][i][ks][1] = q[3];
+          }
+        }
+    }
+    const int col = cb + 8 * t4;
+#pragma unroll
+    for (int mt = 0; mt < MTU; ++mt) {
+      if (mt * 16 >= tile.rows) break;
+      const int m0 = mt * 16 + g, m1 = m0 + 8;
+      const bool ok0 = m0 < tile.rows && col < o_end, ok1 = m1 < tile.rows && col < o_end;
+      uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+      if (a.base) {
+        if (ok0) b0 = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m0) * a.ldbase + col);
+        if (ok1) b1 = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m1) * a.ldbase + col);
+      }
+      float d[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KC; ++i) {
+        if (32 * i >= r_a) break;
+        uint32_t fh[KS][4], fl[KS][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // rows g, g + 8
+          const int m = mt * 16 + half * 8 + g;
+          if (KS == 2) {
+            int c = 4 * i + t4;
+            if (RP >= 64) c ^= (m & 1) << 2;
+            const uint32_t at = tbase + m * RP * 2 + c * 16;
+            const uint4 h = lds_v4(at), l = lds_v4(at + BM * RP * 2);
+            fh[0][half] = h.x;
+            fh[0][2 + half] = h.y;
+            fh[KS - 1][half] = h.z;
+            fh[KS - 1][2 + half] = h.w;
+            fl[0][half] = l.x;
+            fl[0][2 + half] = l.y;
+            fl[KS - 1][half] = l.z;
+            fl[KS - 1][2 + half] = l.w;
+          } else {
+            const uint32_t at = tbase + m * RP * 2 + t4 * 8;
+            const uint2 h = lds_v2(at), l = lds_v2(at + BM * RP * 2);
+            fh[0][half] = h.x;
+            fh[0][2 + half] = h.y;
+            fl[0][half] = l.x;
+            fl[0][2 + half] = l.y;
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t h0, l0, h1, l1;
+            pool_parts<XT>(w[j][i][ks][0], h0, l0);
+            pool_parts<XT>(w[j][i][ks][1], h1, l1);
+            MmaT<1>::mma(d[j], fh[ks], h0, h1);
+            MmaT<1>::mma(d[j], fl[ks], h0, h1);
+            if (XT == 0) MmaT<1>::mma(d[j], fh[ks], l0, l1);
+          }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int m = half ? m1 : m0;
+        if (!(half ? ok1 : ok0)) continue;
+        const uint4 b = half ? b1 : b0;
+        uint32_t bw[4] = {b.x, b.y, b.z, b.w}, ow[4];
+        uint4 keep = make_uint4(0, 0, 0, 0);
+        if (UP == 1 && drop) keep = drop_block(dst, (uint32_t)col >> 3, (uint32_t)(tile.row0 + m));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v0 = d[j][2 * half], v1 = d[j][2 * half + 1];
+          if (UP == 1 && drop) {
+            v0 = drop_keep(keep, 2 * j, dst.thr_hi) ? v0 * out_scale : 0.0f;
+            v1 = drop_keep(keep, 2 * j + 1, dst.thr_hi) ? v1 * out_scale : 0.0f;
+          }
+          const float2 bf = Elem<XT>::pair(bw[j]);
+          ow[j] = (uint32_t)Elem<XT>::from_float(bf.x + v0) | ((uint32_t)Elem<XT>::from_float(bf.y + v1) << 16);
+        }
+        *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// weight gradients
+// ---------------------------------------------------------------------------
+//   dA[a] = sum_m dt[m]^T drop(x)[m]        [R, K]
+//   dB[a] = sum_m s_a dy[m]^T t[m]          [N, R]
+// Both are G[r, c] = sum_m P[m, r] X[m, c] over the rows of the adapter's
+// segments, P fp32 and X 16-bit; dB is stored transposed.  One launch does
+// both: a cluster owns 32 NT columns of one adapter's dA or dB and its CTAs
+// take the adapter's row tiles in turn; their fp32 sums meet in distributed
+// shared memory in rank order.  An adapter that occurs in several segments is
+// summed over all of them by the same cluster, so there are no atomics and no
+// partial gradients in global memory.  P enters as two bf16 parts (relative
+// error below 2^-17), fp16 X as two exact bf16 parts.
+
+struct LoraWgradSide {
+  const uint16_t *X;  // [M, C] rows of stride ldx
+  const float *P;     // [M, R]
+  float *out;         // dA [L, R, C], or dB [L, C, R]
+  int64_t ldx;
+  int C;
+  int tiles;          // column tiles; 0 if this gradient is not wanted
+};
+
+struct LoraWgradArgs {
+  LoraWgradSide dA, dB;
+  const int *ranks;
+  const float *scales;
+  const int *seg_off, *seg_adapter;
+  int64_t M;
+  int R, L, S, CS;
+  DropArgs drop;  // on dA's X
+};
+
+template <int RP> struct WgradGeom {
+  static constexpr int BK = 64;                    // rows per step
+  static constexpr int NT = (RP == 128) ? 2 : 4;   // 8-column tiles per warp
+  static constexpr int CG = 4, MH = kLoraWarps / CG;  // column groups, warps sharing a step's rows
+  static constexpr int CT = CG * 8 * NT;           // columns per CTA
+  static constexpr int XST = 3, PST = 2;           // stages of X and P
+  static constexpr int X_BYTES = BK * CT * 2;
+  static constexpr int P_BYTES = 2 * BK * RP * 2;  // two parts
+  static constexpr int PARTIAL = MH * RP * CT * 4;
+  static constexpr int RING = XST * X_BYTES + PST * P_BYTES;
+  static constexpr int MAIN = RING > PARTIAL ? RING : PARTIAL;
+  static constexpr int TOTAL = MAIN + RP * CT * 4;
+};
+
+// The row tiles of one adapter, in order: every CTA walks all of them and
+// takes those whose number is its rank modulo CS.
+struct WgradRows {
+  int s0;            // first segment of the warp's 32
+  unsigned mask;     // segments of the 32 that are left
+  int start, len;    // this lane's segment
+  int cur, cur_len;  // segment being cut: next row, rows left
+  int count;         // tiles passed
+};
+
+template <int BK> BQ_DEV bool wgrad_next(WgradRows &w, const LoraWgradArgs &a, int adapter, int rank, int *row0, int *rows) {
+  const int lane = threadIdx.x & 31;
+  while (true) {
+    while (w.cur_len <= 0) {
+      while (!w.mask) {
+        if (w.s0 >= a.S) return false;
+        const int s = w.s0 + lane;
+        bool hit = false;
+        w.len = 0;
+        if (s < a.S && a.seg_adapter[s] == adapter) {
+          w.len = lora_segment(a.seg_off, s, a.M, &w.start);
+          hit = w.len > 0;
+        }
+        w.mask = __ballot_sync(0xffffffffu, hit);
+        w.s0 += 32;
+      }
+      const int src = __ffs(w.mask) - 1;
+      w.mask &= w.mask - 1;
+      w.cur = __shfl_sync(0xffffffffu, w.start, src);
+      w.cur_len = __shfl_sync(0xffffffffu, w.len, src);
+    }
+    // tiles count .. count + n - 1 are this segment's; skip to this CTA's
+    const int skip = (rank - w.count % a.CS + a.CS) % a.CS;
+    const int n = (w.cur_len + BK - 1) / BK;
+    if (skip >= n) {
+      w.count += n;
+      w.cur_len = 0;
+      continue;
+    }
+    *row0 = w.cur + skip * BK;
+    *rows = min(BK, w.cur_len - skip * BK);
+    w.count += skip + 1;
+    w.cur += (skip + 1) * BK;
+    w.cur_len -= (skip + 1) * BK;
+    return true;
+  }
+}
+
+// 16-byte chunk c of row m of an X stage (CT columns) / of a P part (RP ranks):
+// the eight consecutive rows of a transposed fragment lie in different banks.
+template <int W> BQ_DEV uint32_t wgrad_offset(int m, int c) {
+  int f;
+  if (W >= 64) f = m & 7;
+  else if (W == 32) f = (m >> 1) & 3;
+  else f = (m >> 2) & 1;
+  return (uint32_t)(m * W * 2 + ((c ^ f) << 4));
+}
+
+// grid = CS x (L x (dA tiles + dB tiles)), cluster = (CS, 1, 1).
+template <int XT, int RP>
+__global__ void __launch_bounds__(kLoraThreads, (RP == 128 || XT == 0) ? 1 : 2)
+lora_wgrad_kernel(LoraWgradArgs a) {
+  using G = WgradGeom<RP>;
+  constexpr int BK = G::BK, NT = G::NT, CT = G::CT, MR = RP / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CS = a.CS, rank = (int)blockIdx.x % CS;
+  const int work = (int)blockIdx.x / CS, per_adapter = a.dA.tiles + a.dB.tiles;
+  const int adapter = work / per_adapter;
+  const bool is_b = work % per_adapter >= a.dA.tiles;
+  const LoraWgradSide side = is_b ? a.dB : a.dA;
+  const int c0 = (work % per_adapter - (is_b ? a.dA.tiles : 0)) * CT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int cgrp = warp % G::CG, mh = warp / G::CG;
+  const uint32_t sbase = smem_u32(smem);
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+  const bool masked = !is_b && a.drop.thr != 0;
+  const DropState dst = drop_state(a.drop);
+  const int r_a = lora_rank(a.ranks, adapter, a.L, a.R);
+  const int m_tiles = (r_a + 15) / 16;
+
+  // X chunks and P quads of this thread
+  constexpr int XCH = CT / 8, XPT = BK * XCH / kLoraThreads;
+  constexpr int PQ = RP / 4, PPT = BK * PQ / kLoraThreads;
+  static_assert(BK * XCH % kLoraThreads == 0 && BK * PQ % kLoraThreads == 0, "uneven staging");
+  WgradRows ahead = {0, 0u, 0, 0, 0, 0, 0};
+  int row_of[G::XST], rows_of[G::XST];  // tile in each X stage; rows 0: none
+  float4 pv[PPT];
+
+  auto load_x = [&](int st, int row0, int rows) {
+    const uint32_t stage = sbase + st * G::X_BYTES;
+#pragma unroll
+    for (int k = 0; k < XPT; ++k) {
+      const int i = threadIdx.x + k * kLoraThreads, m = i / XCH, c = i % XCH;
+      const bool ok = m < rows && c0 + 8 * c < side.C;
+      cp_async16(stage + wgrad_offset<CT>(m, c), ok ? side.X + (int64_t)(row0 + m) * side.ldx + c0 + 8 * c : side.X, ok);
+    }
+  };
+  auto load_p = [&](int row0, int rows) {
+#pragma unroll
+    for (int k = 0; k < PPT; ++k) {
+      const int i = threadIdx.x + k * kLoraThreads, m = i / PQ, r = 4 * (i % PQ);
+      pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (m < rows && r < r_a) pv[k] = *reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r);
+    }
+  };
+  auto store_p = [&](int st) {
+    const uint32_t stage = sbase + G::XST * G::X_BYTES + st * G::P_BYTES;
+#pragma unroll
+    for (int k = 0; k < PPT; ++k) {
+      const int i = threadIdx.x + k * kLoraThreads, m = i / PQ, r = 4 * (i % PQ);
+      const float4 v = pv[k];
+      uint32_t h0, l0, h1, l1;
+      split_bf16(v.x, r + 1 < r_a ? v.y : 0.0f, h0, l0);
+      split_bf16(r + 2 < r_a ? v.z : 0.0f, r + 3 < r_a ? v.w : 0.0f, h1, l1);
+      const uint32_t at = stage + wgrad_offset<RP>(m, r >> 3) + (r & 7) * 2;
+      asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
+      asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + BK * RP * 2), "r"(l0), "r"(l1) : "memory");
+    }
+  };
+
+  float acc[MR][NT][4];
+#pragma unroll
+  for (int i = 0; i < MR; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
+
+  bool more = r_a > 0;
+  auto fetch = [&](int st) {  // the next tile into X stage st
+    rows_of[st] = 0;
+    if (more) {
+      more = wgrad_next<BK>(ahead, a, adapter, rank, &row_of[st], &rows_of[st]);
+      if (!more) rows_of[st] = 0;
+      else load_x(st, row_of[st], rows_of[st]);
+    }
+    cp_async_commit();
+  };
+  fetch(0);
+  fetch(1);
+  if (rows_of[0] > 0) load_p(row_of[0], rows_of[0]);
+  // stage numbers are compile-time constants: three steps a turn
+  auto run_step = [&](int st, int nst, int fst, int pst) {
+    const int row0 = row_of[st], rows = rows_of[st];
+    store_p(pst);
+    if (rows_of[nst] > 0) load_p(row_of[nst], rows_of[nst]);
+    cp_async_wait<1>();
+    if (masked) {  // each thread masks the chunks that it copied
+      const uint32_t stage = sbase + st * G::X_BYTES;
+#pragma unroll
+      for (int k = 0; k < XPT; ++k) {
+        const int i = threadIdx.x + k * kLoraThreads, m = i / XCH, c = i % XCH;
+        if (m < rows) {
+          const uint32_t at = stage + wgrad_offset<CT>(m, c);
+          uint4 v = lds_v4(at);
+          const uint4 kp = drop_mask8(drop_block(dst, (uint32_t)(c0 / 8 + c), (uint32_t)(row0 + m)), dst.thr_hi);
+          v.x &= kp.x;
+          v.y &= kp.y;
+          v.z &= kp.z;
+          v.w &= kp.w;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        }
+      }
+    }
+    __syncthreads();
+    fetch(fst);
+    const uint32_t xs = sbase + st * G::X_BYTES, ps = sbase + G::XST * G::X_BYTES + pst * G::P_BYTES;
+    const int l8 = lane & 7, m1 = (lane >> 3) & 1, m2 = lane >> 4;
+#pragma unroll
+    for (int kk = 0; kk < BK / 16 / G::MH; ++kk) {
+      const int k0 = (kk * G::MH + mh) * 16;
+      if (k0 >= rows) continue;
+      uint32_t bf[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; j += 2) {  // matrices (j, low), (j, high), (j + 1, low), (j + 1, high)
+        uint32_t q[4];
+        ldmatrix_x4_trans(q, xs + wgrad_offset<CT>(k0 + l8 + 8 * m1, cgrp * NT + j + m2));
+        bf[j][0] = q[0];
+        bf[j][1] = q[1];
+        bf[j + 1][0] = q[2];
+        bf[j + 1][1] = q[3];
+      }
+      uint32_t bl[NT][2];
+      if (XT == 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          pool_parts<XT>(bf[j][0], bf[j][0], bl[j][0]);
+          pool_parts<XT>(bf[j][1], bf[j][1], bl[j][1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MR; ++i) {
+        if (i >= m_tiles) break;
+        // matrices (ranks low, rows low), (high, low), (low, high), (high, high)
+        uint32_t ph[4], pl[4];
+        const uint32_t at = ps + wgrad_offset<RP>(k0 + l8 + 8 * m2, 2 * i + m1);
+        ldmatrix_x4_trans(ph, at);
+        ldmatrix_x4_trans(pl, at + BK * RP * 2);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          MmaT<1>::mma(acc[i][j], ph, bf[j][0], bf[j][1]);
+          MmaT<1>::mma(acc[i][j], pl, bf[j][0], bf[j][1]);
+          if (XT == 0) MmaT<1>::mma(acc[i][j], ph, bl[j][0], bl[j][1]);
+        }
+      }
+    }
+  };
+  int pst = 0;
+  while (rows_of[0] > 0) {
+    run_step(0, 1, 2, pst);
+    pst ^= 1;
+    if (rows_of[1] <= 0) break;
+    run_step(1, 2, 0, pst);
+    pst ^= 1;
+    if (rows_of[2] <= 0) break;
+    run_step(2, 0, 1, pst);
+    pst ^= 1;
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  float *part = reinterpret_cast<float *>(smem);  // [MH][RP][CT]
+#pragma unroll
+  for (int i = 0; i < MR; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float *p = part + (mh * RP + i * 16 + g) * CT + (cgrp * NT + j) * 8 + 2 * t4;
+      *reinterpret_cast<float2 *>(p) = make_float2(acc[i][j][0], acc[i][j][1]);
+      *reinterpret_cast<float2 *>(p + 8 * CT) = make_float2(acc[i][j][2], acc[i][j][3]);
+    }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  const int per = RP * CT / CS;
+  float *recv = reinterpret_cast<float *>(smem + G::MAIN);  // [CS][per]
+  for (int e = 4 * (int)threadIdx.x; e < RP * CT; e += 4 * kLoraThreads) {
+    float4 s = *reinterpret_cast<const float4 *>(part + e);
+#pragma unroll
+    for (int q = 1; q < G::MH; ++q) {
+      const float4 v = *reinterpret_cast<const float4 *>(part + q * RP * CT + e);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    const int owner = e / per;
+    *reinterpret_cast<float4 *>(cluster.map_shared_rank(recv, owner) + rank * per + (e - owner * per)) = s;
+  }
+  cluster.sync();
+  const float scale = is_b ? (r_a > 0 ? a.scales[adapter] : 0.0f) : (masked ? a.drop.inv_keep : 1.0f);
+  auto total = [&](int e) {  // element e of this CTA's share
+    float v = 0.0f;
+    for (int q = 0; q < CS; ++q) v += recv[q * per + e];
+    return v != 0.0f ? v * scale : 0.0f;  // an unused adapter's gradient is 0 whatever its scale
+  };
+  if (!is_b) {
+    for (int i = threadIdx.x; i < per; i += kLoraThreads) {
+      const int e = rank * per + i, r = e / CT, c = c0 + e % CT;
+      if (r < a.R && c < side.C) side.out[((int64_t)adapter * a.R + r) * side.C + c] = r < r_a ? total(i) : 0.0f;
+    }
+  } else {
+    // transposed: consecutive threads take consecutive ranks of one column
+    const int r0 = rank * per / CT, nr = per / CT;  // whole ranks (CS divides RP)
+    for (int i = threadIdx.x; i < per; i += kLoraThreads) {
+      const int c = i / nr, r = i % nr;
+      if (r0 + r < a.R && c0 + c < side.C)
+        side.out[((int64_t)adapter * side.C + c0 + c) * a.R + r0 + r] = r0 + r < r_a ? total(r * CT + c) : 0.0f;
+    }
+  }
+}
+
+}  // namespace bq

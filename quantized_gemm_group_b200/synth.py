@@ -90,6 +90,16 @@ def activations(M: int, K: int, seed: int, dtype: str = "bf16", device="cpu") ->
     return normal((M, K), 1.0, seed, dtype, device)
 
 
+def adapters(L: int, R: int, K: int, N: int, seed: int, dtype: str = "bf16", device="cpu", ranks=None):
+    """A pool of L low-rank adapters of rank R (or the given ranks): A [L, R, K] ~ N(0, 1/K), B [L, N, R] ~
+    N(0, 0.05), ranks int32 [L], scales fp32 [L]."""
+    A = normal((L * R, K), K ** -0.5, seed, dtype, device).view(L, R, K)
+    B = normal((L * N, R), 0.05, seed + 1, dtype, device).view(L, N, R)
+    rk = torch.tensor([R] * L if ranks is None else list(ranks), dtype=torch.int32, device=device)
+    scales = torch.tensor([2.0 / (1 + i % 3) for i in range(L)], dtype=torch.float32, device=device)
+    return A, B, rk, scales
+
+
 def bits16(t: torch.Tensor) -> np.ndarray:
     """uint16 bit patterns of an fp16/bf16 tensor, on the host."""
     return t.detach().cpu().contiguous().view(torch.int16).numpy().view(np.uint16)
