@@ -16,6 +16,7 @@
 #include "gemm.cuh"
 #include "gemv.cuh"
 #include "lora.cuh"
+#include "lora_tc.cuh"
 #include "quantize.cuh"
 #include "selftest.cuh"
 
@@ -891,12 +892,13 @@ bq_status launch_dropout(const void *x, int64_t rows, int64_t cols, int64_t ldx,
 }
 
 // Launch with clusters of cs CTAs along x; overlap: programmatic dependent launch.
-template <typename Kern, typename Args>
-bq_status launch_cluster(Kern kern, int64_t grid, int cs, int smem, bool overlap, const Args &a, cudaStream_t st) {
+template <typename... Params, typename... Args>
+bq_status launch_cluster(void (*kern)(Params...), int64_t grid, int cs, int threads, int smem, bool overlap,
+                         cudaStream_t st, const Args &...args) {
   if (grid > 0x7fffffffll) return BQ_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kLoraThreads, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attrs[2];
@@ -908,7 +910,7 @@ bq_status launch_cluster(Kern kern, int64_t grid, int cs, int smem, bool overlap
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = overlap ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
     cudaGetLastError();
     return BQ_ERR_CUDA;
   }
@@ -917,48 +919,92 @@ bq_status launch_cluster(Kern kern, int64_t grid, int cs, int smem, bool overlap
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-template <int XT, int UP, int BM, int RP>
+// A [d2, d1, d0] 16-bit tensor (rows of s1 elements, planes of s2; d2 = 0: a
+// matrix) as a tensor map with boxes of b0 x b1, 128-byte swizzle, zero fill.
+bool make_map(CUtensorMap *map, const void *base, bool bf16, int64_t d0, int64_t d1, int64_t d2, int64_t s1, int64_t s2,
+              int b0, int b1) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+  const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, d2 > 0 ? 3 : 2,
+             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of bm rows that S segments of M rows can need.
+int64_t lora_tiles(const LoraArgs &a, int bm) {
+  const int64_t cut = a.M / bm + a.S;
+  return cut < a.M ? cut : a.M;
+}
+
+// Short segments: 16-row tiles on mma.sync.
+template <int XT, int UP, int RP>
 bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
-  using G = LoraGeom<BM, RP>;
-  const int64_t cut = a.M / BM + a.S, tiles = cut < a.M ? cut : a.M;
+  using G = LoraGeom<16, RP>;
+  const int64_t tiles = lora_tiles(a, 16);
   // CTAs per tile: as many as keep the grid within a few waves
   int cs = 8;
   while (cs > 1 && tiles * cs > 6 * (int64_t)sm_count()) cs /= 2;
   a.CS = cs;
   a.slice_c = (int)round_up((a.Ci + cs - 1) / cs, G::SC);
   a.slice_o = (int)round_up((a.Co + cs - 1) / cs, 32);
-  constexpr auto kern = lora_kernel<XT, UP, BM, RP>;
+  constexpr auto kern = lora_kernel<XT, UP, 16, RP>;
   if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
-  return launch_cluster(kern, tiles * cs, cs, G::TOTAL, overlap_mode() >= 1, a, st);
+  return launch_cluster(kern, tiles * cs, cs, kLoraThreads, G::TOTAL, overlap_mode() >= 1, st, a);
+}
+
+// Long segments: 128-row tiles on tcgen05.
+template <int XT, int UP, int RP>
+bq_status launch_lora_tc(LoraArgs a, cudaStream_t st) {
+  using G = TcGeom<RP>;
+  CUtensorMap mx = {}, mA = {}, mB = {}, mbase = {};
+  const int64_t K = UP ? a.Co : a.Ci, N = UP ? a.Ci : a.Co;
+  if (!make_map(&mx, a.x, XT == 1, a.Ci, a.M, 0, a.ldx, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
+  if (K && !make_map(&mA, a.A, XT == 1, K, a.R, a.L, K, (int64_t)a.R * K, 64, 16)) return BQ_ERR_CUDA;
+  if (N && !make_map(&mB, a.B, XT == 1, a.R, N, a.L, a.R, (int64_t)a.R * N, 64, 64)) return BQ_ERR_CUDA;
+  if (a.base && a.Co && !make_map(&mbase, a.base, XT == 1, a.Co, a.M, 0, a.ldbase, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
+  a.CS = kTcCS;
+  a.slice_c = (int)round_up((a.Ci + kTcCS - 1) / kTcCS, 64);
+  a.slice_o = (int)round_up((a.Co + kTcCS - 1) / kTcCS, 64);
+  constexpr auto kern = lora_tc_kernel<XT, UP, RP>;
+  if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
+  return launch_cluster(kern, lora_tiles(a, kTcRows) * kTcCS, kTcCS, kTcThreads, G::total, overlap_mode() >= 1, st, mx,
+                        mA, mB, mbase, a);
 }
 
 template <int XT, int UP>
 bq_status launch_lora(const LoraArgs &a, cudaStream_t st) {
-  if (a.M == 0 || a.S == 0) return BQ_OK;
-  const bool small = a.M <= 24 * (int64_t)a.S;  // few rows a segment: 16-row tiles
-  if (a.R <= 16) return small ? launch_lora_t<XT, UP, 16, 16>(a, st) : launch_lora_t<XT, UP, 64, 16>(a, st);
-  if (a.R <= 64) return small ? launch_lora_t<XT, UP, 16, 64>(a, st) : launch_lora_t<XT, UP, 64, 64>(a, st);
-  return small ? launch_lora_t<XT, UP, 16, 128>(a, st) : launch_lora_t<XT, UP, 64, 128>(a, st);
+  if (a.M == 0 || a.S == 0 || a.L == 0) return a.M && a.S ? launch_lora_t<XT, UP, 16>(a, st) : BQ_OK;
+  // few rows a segment (or an empty contraction, which has no tensor map)
+  if (a.M <= 24 * (int64_t)a.S || a.Ci == 0) {
+    if (a.R <= 16) return launch_lora_t<XT, UP, 16>(a, st);
+    return a.R <= 64 ? launch_lora_t<XT, UP, 64>(a, st) : launch_lora_t<XT, UP, 128>(a, st);
+  }
+  return a.R <= 64 ? launch_lora_tc<XT, UP, 64>(a, st) : launch_lora_tc<XT, UP, 128>(a, st);
 }
+
+struct WgradInputs {
+  const void *x, *dy;
+  int64_t ldx, lddy;
+};
 
 template <int XT, int RP>
-bq_status launch_wgrad_t(LoraWgradArgs a, cudaStream_t st) {
+bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, cudaStream_t st) {
   using G = WgradGeom<RP>;
-  if (a.dA.out) a.dA.tiles = (a.dA.C + G::CT - 1) / G::CT;
-  if (a.dB.out) a.dB.tiles = (a.dB.C + G::CT - 1) / G::CT;
+  CUtensorMap mx = {}, mdy = {};
+  if (a.dA.out) a.dA.tiles = (a.dA.C + kWgCols - 1) / kWgCols;
+  if (a.dB.out) a.dB.tiles = (a.dB.C + kWgCols - 1) / kWgCols;
   const int64_t clusters = (int64_t)a.L * (a.dA.tiles + a.dB.tiles);
   if (clusters == 0) return BQ_OK;
-  a.CS = 8;
+  if (a.S && a.dA.tiles && !make_map(&mx, in.x, XT == 1, a.dA.C, a.M, 0, in.ldx, 0, 64, kTcWXBox)) return BQ_ERR_CUDA;
+  if (a.S && a.dB.tiles && !make_map(&mdy, in.dy, XT == 1, a.dB.C, a.M, 0, in.lddy, 0, 64, kTcWXBox)) return BQ_ERR_CUDA;
   constexpr auto kern = lora_wgrad_kernel<XT, RP>;
-  if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
-  return launch_cluster(kern, clusters * a.CS, a.CS, G::TOTAL, false, a, st);
-}
-
-template <int XT>
-bq_status launch_wgrad(const LoraWgradArgs &a, cudaStream_t st) {
-  if (a.R <= 16) return launch_wgrad_t<XT, 16>(a, st);
-  if (a.R <= 64) return launch_wgrad_t<XT, 64>(a, st);
-  return launch_wgrad_t<XT, 128>(a, st);
+  if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
+  return launch_cluster(kern, clusters * kTcCS, kTcCS, kTcThreads, G::total, false, st, mx, mdy, a);
 }
 
 // What bq_lora and bq_lora_grad have in common.
@@ -1088,16 +1134,12 @@ bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int
     s = dtype == BQ_BF16 ? launch_lora<1, 1>(a, st) : launch_lora<0, 1>(a, st);
     if (s != BQ_OK) return s;
   }
-  LoraWgradArgs w = {};
-  w.dA.X = reinterpret_cast<const uint16_t *>(x);
+  WgradArgs w = {};
   w.dA.P = dt;
   w.dA.out = dA;
-  w.dA.ldx = ldx;
   w.dA.C = (int)K;
-  w.dB.X = reinterpret_cast<const uint16_t *>(dy);
   w.dB.P = t;
   w.dB.out = dB;
-  w.dB.ldx = lddy;
   w.dB.C = (int)N;
   w.ranks = ranks;
   w.scales = scales;
@@ -1108,7 +1150,9 @@ bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int
   w.L = L;
   w.S = rows ? S : 0;
   w.drop = a.drop;
-  return dtype == BQ_BF16 ? launch_wgrad<1>(w, st) : launch_wgrad<0>(w, st);
+  const WgradInputs in = {x, dy, M == 1 ? K : ldx, M == 1 ? N : lddy};
+  if (dtype == BQ_BF16) return R <= 64 ? launch_wgrad<1, 64>(w, in, st) : launch_wgrad<1, 128>(w, in, st);
+  return R <= 64 ? launch_wgrad<0, 64>(w, in, st) : launch_wgrad<0, 128>(w, in, st);
 }
 
 }  // extern "C"

@@ -125,6 +125,20 @@ BQ_DEV void lora_check_segments(const int *seg_off, const int *seg_adapter, cons
   if (bad) bq_flag(BQ_FLAG_BADMAP);
 }
 
+// Rows without a contribution: base's (nothing to do in place), t zero.
+BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int o_begin, int o_end, bool with_t, int threads) {
+  const int per = (o_end - o_begin) / 8;  // 16-byte pieces of a row (may be <= 0)
+  if (a.base != a.y)
+    for (int64_t i = threadIdx.x; per > 0 && i < (int64_t)per * tile.rows; i += threads) {
+      const int m = (int)(i / per), c = o_begin + 8 * (int)(i - (int64_t)m * per);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (a.base) v = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m) * a.ldbase + c);
+      *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + c) = v;
+    }
+  if (a.t && with_t)
+    for (int i = threadIdx.x; i < tile.rows * a.R; i += threads) a.t[(int64_t)tile.row0 * a.R + i] = 0.0f;
+}
+
 // The rank to use: 0 (no contribution) without an adapter or with a bad one.
 BQ_DEV int lora_rank(const int *ranks, int adapter, int L, int R) {
   if (adapter < 0 || adapter >= L) return 0;
@@ -238,18 +252,7 @@ lora_kernel(LoraArgs a) {
   const int o_begin = rank * a.slice_o, o_end = min(a.Co, o_begin + a.slice_o);
 
   if (r_a == 0) {
-    // no contribution: the rows are base's (nothing to do in place), t is zero
-    if (a.base != a.y) {
-      const int per = (o_end - o_begin) / 8;  // 16-byte pieces of a row (may be <= 0)
-      for (int i = threadIdx.x; per > 0 && i < per * tile.rows; i += kLoraThreads) {
-        const int m = i / per, c = o_begin + 8 * (i - m * per);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (a.base) v = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m) * a.ldbase + c);
-        *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + c) = v;
-      }
-    }
-    if (a.t && rank == 0)
-      for (int i = threadIdx.x; i < tile.rows * a.R; i += kLoraThreads) a.t[(int64_t)tile.row0 * a.R + i] = 0.0f;
+    lora_copy_rows(a, tile, o_begin, o_end, rank == 0, kLoraThreads);
     return;
   }
   // every CTA has started before any writes into its shared memory
@@ -614,325 +617,6 @@ lora_kernel(LoraArgs a) {
         }
         *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
       }
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// weight gradients
-// ---------------------------------------------------------------------------
-//   dA[a] = sum_m dt[m]^T drop(x)[m]        [R, K]
-//   dB[a] = sum_m s_a dy[m]^T t[m]          [N, R]
-// Both are G[r, c] = sum_m P[m, r] X[m, c] over the rows of the adapter's
-// segments, P fp32 and X 16-bit; dB is stored transposed.  One launch does
-// both: a cluster owns 32 NT columns of one adapter's dA or dB and its CTAs
-// take the adapter's row tiles in turn; their fp32 sums meet in distributed
-// shared memory in rank order.  An adapter that occurs in several segments is
-// summed over all of them by the same cluster, so there are no atomics and no
-// partial gradients in global memory.  P enters as two bf16 parts (relative
-// error below 2^-17), fp16 X as two exact bf16 parts.
-
-struct LoraWgradSide {
-  const uint16_t *X;  // [M, C] rows of stride ldx
-  const float *P;     // [M, R]
-  float *out;         // dA [L, R, C], or dB [L, C, R]
-  int64_t ldx;
-  int C;
-  int tiles;          // column tiles; 0 if this gradient is not wanted
-};
-
-struct LoraWgradArgs {
-  LoraWgradSide dA, dB;
-  const int *ranks;
-  const float *scales;
-  const int *seg_off, *seg_adapter;
-  int64_t M;
-  int R, L, S, CS;
-  DropArgs drop;  // on dA's X
-};
-
-template <int RP> struct WgradGeom {
-  static constexpr int BK = 64;                    // rows per step
-  static constexpr int NT = (RP == 128) ? 2 : 4;   // 8-column tiles per warp
-  static constexpr int CG = 4, MH = kLoraWarps / CG;  // column groups, warps sharing a step's rows
-  static constexpr int CT = CG * 8 * NT;           // columns per CTA
-  static constexpr int XST = 3, PST = 2;           // stages of X and P
-  static constexpr int X_BYTES = BK * CT * 2;
-  static constexpr int P_BYTES = 2 * BK * RP * 2;  // two parts
-  static constexpr int PARTIAL = MH * RP * CT * 4;
-  static constexpr int RING = XST * X_BYTES + PST * P_BYTES;
-  static constexpr int MAIN = RING > PARTIAL ? RING : PARTIAL;
-  static constexpr int TOTAL = MAIN + RP * CT * 4;
-};
-
-// The row tiles of one adapter, in order: every CTA walks all of them and
-// takes those whose number is its rank modulo CS.
-struct WgradRows {
-  int s0;            // first segment of the warp's 32
-  unsigned mask;     // segments of the 32 that are left
-  int start, len;    // this lane's segment
-  int cur, cur_len;  // segment being cut: next row, rows left
-  int count;         // tiles passed
-};
-
-template <int BK> BQ_DEV bool wgrad_next(WgradRows &w, const LoraWgradArgs &a, int adapter, int rank, int *row0, int *rows) {
-  const int lane = threadIdx.x & 31;
-  while (true) {
-    while (w.cur_len <= 0) {
-      while (!w.mask) {
-        if (w.s0 >= a.S) return false;
-        const int s = w.s0 + lane;
-        bool hit = false;
-        w.len = 0;
-        if (s < a.S && a.seg_adapter[s] == adapter) {
-          w.len = lora_segment(a.seg_off, s, a.M, &w.start);
-          hit = w.len > 0;
-        }
-        w.mask = __ballot_sync(0xffffffffu, hit);
-        w.s0 += 32;
-      }
-      const int src = __ffs(w.mask) - 1;
-      w.mask &= w.mask - 1;
-      w.cur = __shfl_sync(0xffffffffu, w.start, src);
-      w.cur_len = __shfl_sync(0xffffffffu, w.len, src);
-    }
-    // tiles count .. count + n - 1 are this segment's; skip to this CTA's
-    const int skip = (rank - w.count % a.CS + a.CS) % a.CS;
-    const int n = (w.cur_len + BK - 1) / BK;
-    if (skip >= n) {
-      w.count += n;
-      w.cur_len = 0;
-      continue;
-    }
-    *row0 = w.cur + skip * BK;
-    *rows = min(BK, w.cur_len - skip * BK);
-    w.count += skip + 1;
-    w.cur += (skip + 1) * BK;
-    w.cur_len -= (skip + 1) * BK;
-    return true;
-  }
-}
-
-// 16-byte chunk c of row m of an X stage (CT columns) / of a P part (RP ranks):
-// the eight consecutive rows of a transposed fragment lie in different banks.
-template <int W> BQ_DEV uint32_t wgrad_offset(int m, int c) {
-  int f;
-  if (W >= 64) f = m & 7;
-  else if (W == 32) f = (m >> 1) & 3;
-  else f = (m >> 2) & 1;
-  return (uint32_t)(m * W * 2 + ((c ^ f) << 4));
-}
-
-// grid = CS x (L x (dA tiles + dB tiles)), cluster = (CS, 1, 1).
-template <int XT, int RP>
-__global__ void __launch_bounds__(kLoraThreads, (RP == 128 || XT == 0) ? 1 : 2)
-lora_wgrad_kernel(LoraWgradArgs a) {
-  using G = WgradGeom<RP>;
-  constexpr int BK = G::BK, NT = G::NT, CT = G::CT, MR = RP / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int CS = a.CS, rank = (int)blockIdx.x % CS;
-  const int work = (int)blockIdx.x / CS, per_adapter = a.dA.tiles + a.dB.tiles;
-  const int adapter = work / per_adapter;
-  const bool is_b = work % per_adapter >= a.dA.tiles;
-  const LoraWgradSide side = is_b ? a.dB : a.dA;
-  const int c0 = (work % per_adapter - (is_b ? a.dA.tiles : 0)) * CT;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int cgrp = warp % G::CG, mh = warp / G::CG;
-  const uint32_t sbase = smem_u32(smem);
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-
-  const bool masked = !is_b && a.drop.thr != 0;
-  const DropState dst = drop_state(a.drop);
-  const int r_a = lora_rank(a.ranks, adapter, a.L, a.R);
-  const int m_tiles = (r_a + 15) / 16;
-
-  // X chunks and P quads of this thread
-  constexpr int XCH = CT / 8, XPT = BK * XCH / kLoraThreads;
-  constexpr int PQ = RP / 4, PPT = BK * PQ / kLoraThreads;
-  static_assert(BK * XCH % kLoraThreads == 0 && BK * PQ % kLoraThreads == 0, "uneven staging");
-  WgradRows ahead = {0, 0u, 0, 0, 0, 0, 0};
-  int row_of[G::XST], rows_of[G::XST];  // tile in each X stage; rows 0: none
-  float4 pv[PPT];
-
-  auto load_x = [&](int st, int row0, int rows) {
-    const uint32_t stage = sbase + st * G::X_BYTES;
-#pragma unroll
-    for (int k = 0; k < XPT; ++k) {
-      const int i = threadIdx.x + k * kLoraThreads, m = i / XCH, c = i % XCH;
-      const bool ok = m < rows && c0 + 8 * c < side.C;
-      cp_async16(stage + wgrad_offset<CT>(m, c), ok ? side.X + (int64_t)(row0 + m) * side.ldx + c0 + 8 * c : side.X, ok);
-    }
-  };
-  auto load_p = [&](int row0, int rows) {
-#pragma unroll
-    for (int k = 0; k < PPT; ++k) {
-      const int i = threadIdx.x + k * kLoraThreads, m = i / PQ, r = 4 * (i % PQ);
-      pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (m < rows && r < r_a) pv[k] = *reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r);
-    }
-  };
-  auto store_p = [&](int st) {
-    const uint32_t stage = sbase + G::XST * G::X_BYTES + st * G::P_BYTES;
-#pragma unroll
-    for (int k = 0; k < PPT; ++k) {
-      const int i = threadIdx.x + k * kLoraThreads, m = i / PQ, r = 4 * (i % PQ);
-      const float4 v = pv[k];
-      uint32_t h0, l0, h1, l1;
-      split_bf16(v.x, r + 1 < r_a ? v.y : 0.0f, h0, l0);
-      split_bf16(r + 2 < r_a ? v.z : 0.0f, r + 3 < r_a ? v.w : 0.0f, h1, l1);
-      const uint32_t at = stage + wgrad_offset<RP>(m, r >> 3) + (r & 7) * 2;
-      asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
-      asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + BK * RP * 2), "r"(l0), "r"(l1) : "memory");
-    }
-  };
-
-  float acc[MR][NT][4];
-#pragma unroll
-  for (int i = 0; i < MR; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
-
-  bool more = r_a > 0;
-  auto fetch = [&](int st) {  // the next tile into X stage st
-    rows_of[st] = 0;
-    if (more) {
-      more = wgrad_next<BK>(ahead, a, adapter, rank, &row_of[st], &rows_of[st]);
-      if (!more) rows_of[st] = 0;
-      else load_x(st, row_of[st], rows_of[st]);
-    }
-    cp_async_commit();
-  };
-  fetch(0);
-  fetch(1);
-  if (rows_of[0] > 0) load_p(row_of[0], rows_of[0]);
-  // stage numbers are compile-time constants: three steps a turn
-  auto run_step = [&](int st, int nst, int fst, int pst) {
-    const int row0 = row_of[st], rows = rows_of[st];
-    store_p(pst);
-    if (rows_of[nst] > 0) load_p(row_of[nst], rows_of[nst]);
-    cp_async_wait<1>();
-    if (masked) {  // each thread masks the chunks that it copied
-      const uint32_t stage = sbase + st * G::X_BYTES;
-#pragma unroll
-      for (int k = 0; k < XPT; ++k) {
-        const int i = threadIdx.x + k * kLoraThreads, m = i / XCH, c = i % XCH;
-        if (m < rows) {
-          const uint32_t at = stage + wgrad_offset<CT>(m, c);
-          uint4 v = lds_v4(at);
-          const uint4 kp = drop_mask8(drop_block(dst, (uint32_t)(c0 / 8 + c), (uint32_t)(row0 + m)), dst.thr_hi);
-          v.x &= kp.x;
-          v.y &= kp.y;
-          v.z &= kp.z;
-          v.w &= kp.w;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-        }
-      }
-    }
-    __syncthreads();
-    fetch(fst);
-    const uint32_t xs = sbase + st * G::X_BYTES, ps = sbase + G::XST * G::X_BYTES + pst * G::P_BYTES;
-    const int l8 = lane & 7, m1 = (lane >> 3) & 1, m2 = lane >> 4;
-#pragma unroll
-    for (int kk = 0; kk < BK / 16 / G::MH; ++kk) {
-      const int k0 = (kk * G::MH + mh) * 16;
-      if (k0 >= rows) continue;
-      uint32_t bf[NT][2];
-#pragma unroll
-      for (int j = 0; j < NT; j += 2) {  // matrices (j, low), (j, high), (j + 1, low), (j + 1, high)
-        uint32_t q[4];
-        ldmatrix_x4_trans(q, xs + wgrad_offset<CT>(k0 + l8 + 8 * m1, cgrp * NT + j + m2));
-        bf[j][0] = q[0];
-        bf[j][1] = q[1];
-        bf[j + 1][0] = q[2];
-        bf[j + 1][1] = q[3];
-      }
-      uint32_t bl[NT][2];
-      if (XT == 0) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          pool_parts<XT>(bf[j][0], bf[j][0], bl[j][0]);
-          pool_parts<XT>(bf[j][1], bf[j][1], bl[j][1]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < MR; ++i) {
-        if (i >= m_tiles) break;
-        // matrices (ranks low, rows low), (high, low), (low, high), (high, high)
-        uint32_t ph[4], pl[4];
-        const uint32_t at = ps + wgrad_offset<RP>(k0 + l8 + 8 * m2, 2 * i + m1);
-        ldmatrix_x4_trans(ph, at);
-        ldmatrix_x4_trans(pl, at + BK * RP * 2);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          MmaT<1>::mma(acc[i][j], ph, bf[j][0], bf[j][1]);
-          MmaT<1>::mma(acc[i][j], pl, bf[j][0], bf[j][1]);
-          if (XT == 0) MmaT<1>::mma(acc[i][j], ph, bl[j][0], bl[j][1]);
-        }
-      }
-    }
-  };
-  int pst = 0;
-  while (rows_of[0] > 0) {
-    run_step(0, 1, 2, pst);
-    pst ^= 1;
-    if (rows_of[1] <= 0) break;
-    run_step(1, 2, 0, pst);
-    pst ^= 1;
-    if (rows_of[2] <= 0) break;
-    run_step(2, 0, 1, pst);
-    pst ^= 1;
-  }
-  cp_async_wait<0>();
-  __syncthreads();
-
-  float *part = reinterpret_cast<float *>(smem);  // [MH][RP][CT]
-#pragma unroll
-  for (int i = 0; i < MR; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float *p = part + (mh * RP + i * 16 + g) * CT + (cgrp * NT + j) * 8 + 2 * t4;
-      *reinterpret_cast<float2 *>(p) = make_float2(acc[i][j][0], acc[i][j][1]);
-      *reinterpret_cast<float2 *>(p + 8 * CT) = make_float2(acc[i][j][2], acc[i][j][3]);
-    }
-  __syncthreads();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  const int per = RP * CT / CS;
-  float *recv = reinterpret_cast<float *>(smem + G::MAIN);  // [CS][per]
-  for (int e = 4 * (int)threadIdx.x; e < RP * CT; e += 4 * kLoraThreads) {
-    float4 s = *reinterpret_cast<const float4 *>(part + e);
-#pragma unroll
-    for (int q = 1; q < G::MH; ++q) {
-      const float4 v = *reinterpret_cast<const float4 *>(part + q * RP * CT + e);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    const int owner = e / per;
-    *reinterpret_cast<float4 *>(cluster.map_shared_rank(recv, owner) + rank * per + (e - owner * per)) = s;
-  }
-  cluster.sync();
-  const float scale = is_b ? (r_a > 0 ? a.scales[adapter] : 0.0f) : (masked ? a.drop.inv_keep : 1.0f);
-  auto total = [&](int e) {  // element e of this CTA's share
-    float v = 0.0f;
-    for (int q = 0; q < CS; ++q) v += recv[q * per + e];
-    return v != 0.0f ? v * scale : 0.0f;  // an unused adapter's gradient is 0 whatever its scale
-  };
-  if (!is_b) {
-    for (int i = threadIdx.x; i < per; i += kLoraThreads) {
-      const int e = rank * per + i, r = e / CT, c = c0 + e % CT;
-      if (r < a.R && c < side.C) side.out[((int64_t)adapter * a.R + r) * side.C + c] = r < r_a ? total(i) : 0.0f;
-    }
-  } else {
-    // transposed: consecutive threads take consecutive ranks of one column
-    const int r0 = rank * per / CT, nr = per / CT;  // whole ranks (CS divides RP)
-    for (int i = threadIdx.x; i < per; i += kLoraThreads) {
-      const int c = i / nr, r = i % nr;
-      if (r0 + r < a.R && c0 + c < side.C)
-        side.out[((int64_t)adapter * side.C + c0 + c) * a.R + r0 + r] = r0 + r < r_a ? total(r * CT + c) : 0.0f;
     }
   }
 }

@@ -1,0 +1,1032 @@
+// lora_tc.cuh -- low-rank adapters on the 5th-generation tensor cores, for
+// segments of many rows (the kernel of lora.cuh takes short ones), and their
+// weight gradients.  The operands' formulas are in lora.cuh.
+//
+// What bounds it is memory; mma.sync spent about 15 instructions for every
+// matrix instruction on addresses, fragments and partial sums and reached a
+// third of the copy rate (8192 rows, 14336 -> 4096, rank 64: 180 us, gradients
+// of 4096 -> 14336 510 us).  Here tiles come by TMA, tcgen05.mma reads them from shared
+// memory, and threads touch only t, the masks and the output.
+//
+// lora_tc_kernel: a cluster of 8 CTAs owns 128 rows of one segment.  Each
+// contracts an eighth of the columns into tensor memory (down), sends its
+// partial sums to the CTA that owns the row (16 rows each, distributed shared
+// memory, added in rank order: the same bits every time), the owner sends the
+// 16-bit parts of t to all eight, and each writes an eighth of the output
+// columns (up).  Two CTAs fit an SM, so one's exchange hides behind the
+// other's streams.  Roles (10 warps): warp 0 producer (one ring of slots: a
+// chunk of x and of the down pool, later a chunk of base and of the up pool);
+// warp 1 issues tcgen05.mma; warps 2-9 (two per TMEM lane quadrant) mask x,
+// exchange the sums and finish the output.
+//
+// Rounding: t enters the up product as two 16-bit parts, t = hi + lo (bf16:
+// relative error below 2^-17; fp16: the row is first scaled by a power of two so
+// that its largest value lies in [2^14, 2^15), error below 2^-22 of it).  One
+// part would lose 2^-9; the second costs a matrix instruction and no traffic.
+//
+// What lies outside never enters a product: columns behind K, N or R are
+// zero-filled by TMA (the pools are 3D maps, so an adapter's end is an edge),
+// ranks behind an adapter's rank are zeroed in shared memory where they share
+// a k-step of 16 with used ones, and rows behind a segment's end only reach
+// output rows that are not stored (weight gradients: they are zeroed).
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+#include "dropout.cuh"
+#include "gemm.cuh"
+#include "lora.cuh"
+
+namespace bq {
+
+constexpr int kTcCS = 8;                       // CTAs per cluster
+constexpr int kTcRows = 128;                   // rows per tile (MMA M)
+constexpr int kTcOwn = kTcRows / kTcCS;        // rows whose sums one CTA owns
+constexpr int kTcWorkers = 8;                  // worker warps
+constexpr int kTcThreads = 32 * (2 + kTcWorkers);
+constexpr int kTcXBox = 32;                    // rows per TMA box of x and base
+constexpr int kTcWXBox = 16;                   // rows per TMA box of the weight gradients' X
+
+// ---------------------------------------------------------------------------
+// primitives
+// ---------------------------------------------------------------------------
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: 8-row groups
+// SBO = 1024 bytes apart.  MN-major (rows run along the contraction, 64
+// elements of the other index in a row): 8-row groups SBO = 1024 bytes
+// apart, blocks of 64 elements LBO bytes apart.
+BQ_DEV uint64_t tc_desc(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+// Instruction descriptor (see gemm_idesc): M = 128, fp32 accumulation, both
+// operands of type XT; MN-major operands set bit 15 (A) / 16 (B).
+template <int XT> BQ_DEV uint32_t tc_idesc(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((uint32_t)XT << 7) | ((uint32_t)XT << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);
+}
+BQ_DEV void tc_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+BQ_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+// Arrive on the mbarrier at this shared-memory address of CTA `cta` of the cluster.
+BQ_DEV void mbar_arrive_cta(uint32_t bar, uint32_t cta) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar),
+      "r"(cta)
+      : "memory");
+}
+BQ_DEV bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+BQ_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+BQ_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+BQ_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+BQ_DEV void sts_v4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// 32 consecutive fp32 columns of this thread's TMEM lane, not yet waited for.
+BQ_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Two floats as the hi and lo parts of type XT (fp16: scaled by the caller).
+template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t &lo) {
+  if (XT == 1) {
+    split_bf16(a, b, hi, lo);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    float ra = a - f.x, rb = b - f.y;
+    if (!(fabsf(ra) <= 3.402823466e38f)) ra = 0.0f;
+    if (!(fabsf(rb) <= 3.402823466e38f)) rb = 0.0f;
+    const __half2 l = __floats2half2_rn(ra, rb);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+  }
+}
+// 2^e that brings a largest magnitude m into [2^14, 2^15) when divided by it
+// (1 where m is 0 or not finite), as the pair (2^e, 2^-e).
+BQ_DEV float2 tc_scale(float m) {
+  if (!(m > 0.0f) || !(m <= 3.402823466e38f)) return make_float2(1.0f, 1.0f);
+  int e = (int)(__float_as_uint(m) >> 23) - 127 - 14;
+  e = max(-126, min(e, 126));
+  return make_float2(__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23));
+}
+
+// ---------------------------------------------------------------------------
+// forward / input gradient
+// ---------------------------------------------------------------------------
+
+template <int RP> struct TcGeom {
+  static constexpr int X_BYTES = kTcRows * 128;     // 128 rows x 64 columns
+  static constexpr int W_BYTES = RP * 128;          // 64 x RP of a pool
+  static constexpr int SLOT = X_BYTES + W_BYTES;
+  static constexpr int NS = (RP == 64) ? 3 : 4;     // two CTAs per SM / one
+  static constexpr int BLOCKS = RP / 64;            // 64-rank blocks
+  static constexpr int T_BYTES = 2 * BLOCKS * kTcRows * 128;  // hi and lo; the sums' buffer before
+  static constexpr int TOTAL0 = NS * SLOT + T_BYTES;
+  static constexpr int bar_off = TOTAL0;
+  static constexpr int nbar = 4 * NS + 10;
+  static constexpr int scale_off = bar_off + 8 * nbar;  // fp32 per row
+  static constexpr int tmem_off = scale_off + 4 * kTcRows;
+  static constexpr int abort_off = tmem_off + 4;
+  static constexpr int total = abort_off + 4 + 1024;
+  static constexpr int TM_COLS = 256;               // P: RP columns, output: 2 x 64
+  static constexpr int PER_THREAD = kTcOwn * RP / 4 / (32 * kTcWorkers);  // owned quads (at least 1)
+};
+
+struct TcBars {
+  uint32_t full, masked, free_mma, free_out;  // [NS]
+  uint32_t p_full, d_full, d_empty;           // 1, [2], [2]
+  uint32_t recv, taken, t_in, t_ready, done;
+  BQ_DEV TcBars(uint32_t base, int ns) {
+    full = base;
+    masked = full + 8u * ns;
+    free_mma = masked + 8u * ns;
+    free_out = free_mma + 8u * ns;
+    p_full = free_out + 8u * ns;
+    d_full = p_full + 8u;
+    d_empty = d_full + 16u;
+    recv = d_empty + 16u;
+    taken = recv + 8u;
+    t_in = taken + 8u;
+    t_ready = t_in + 8u;
+    done = t_ready + 8u;
+  }
+};
+
+// Worker warps (two per TMEM lane quadrant, thread = row of the tile).
+template <int XT, int UP, int RP>
+BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, int r16, int D, int U, bool patch, bool pad,
+                            int o_begin, int o_end, int c_begin, int rank, uint32_t tmem, uint32_t sbase,
+                            unsigned char *smem, const TcBars &B, volatile int *abort, cg::cluster_group &cluster) {
+  using G = TcGeom<RP>;
+  constexpr int NS = G::NS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = (int)threadIdx.x - 64;
+  const int quad = warp & 3, half = (warp - 2) >> 2, m = quad * 32 + lane;
+  const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+  const bool drop = a.drop.thr != 0;
+  const DropState dst = drop_state(a.drop);
+  bool ok = true;
+  auto vote = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+
+  // ---- down: masks on x ----------------------------------------------------
+  if (patch)
+    for (int s = 0; s < D && ok; ++s) {
+      const int slot = s % NS;
+      ok = vote(!*abort && mbar_wait(B.full + 8u * slot, (s / NS) & 1));
+      if (!ok) break;
+      if (UP == 0 && drop) {
+        const uint32_t xs = sbase + slot * G::SLOT;
+#pragma unroll
+        for (int k = 0; k < kTcRows * 8 / (32 * kTcWorkers); ++k) {
+          const int i = wt + k * 32 * kTcWorkers, row = i >> 3, c = i & 7;
+          if (row >= tile.rows) continue;
+          const uint4 g = drop_mask8(drop_block(dst, (uint32_t)((c_begin >> 3) + 8 * s + c), (uint32_t)(tile.row0 + row)),
+                                     dst.thr_hi);
+          const uint32_t at = xs + row * 128 + ((c ^ (row & 7)) << 4);
+          uint4 v = lds_v4(at);
+          v.x &= g.x;
+          v.y &= g.y;
+          v.z &= g.z;
+          v.w &= g.w;
+          sts_v4(at, v);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.masked + 8u * slot);
+    }
+
+  // ---- the sums meet -------------------------------------------------------
+  // partial sums go to the owner of the row: [source CTA][16 rows][RP], 16-byte
+  // chunks XORed with the row so that a warp's rows lie in different banks
+  float *recv = reinterpret_cast<float *>(smem + NS * G::SLOT);
+  if (ok && D > 0) {
+    ok = vote(mbar_wait(B.p_full, 0));
+    tc_fence_after();
+  }
+  if (ok) {
+    const int rr = rank * kTcOwn + m % kTcOwn;
+    float *to = cluster.map_shared_rank(recv, m / kTcOwn) + rr * RP;
+    for (int cgp = half; cgp < r16 / 16; cgp += 2) {
+      float v[16];
+      if (D > 0) {
+        tmem_ld16(tmem + lane_addr + cgp * 16, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4 *>(to + 4 * ((cgp * 4 + q) ^ (rr & 7))) =
+            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+    __syncwarp();
+    if (lane < kTcCS) mbar_arrive_cta(B.recv, lane);
+    ok = vote(mbar_wait_cluster(B.recv, 0));
+  }
+  float own[G::PER_THREAD][4];
+  if (ok) {
+    const float sc = a.scales[tile.adapter];
+    const float pre = (UP == 0) ? a.drop.inv_keep : sc;  // to t (or dt) as stored
+#pragma unroll
+    for (int k = 0; k < G::PER_THREAD; ++k) {
+      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), chunk = i % (RP / 4), r = 4 * chunk;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (r < r_a)
+        for (int q = 0; q < kTcCS; ++q) {
+          const int rr = q * kTcOwn + ml;
+          const float4 p = *reinterpret_cast<const float4 *>(recv + rr * RP + 4 * (chunk ^ (rr & 7)));
+          v[0] += p.x;
+          v[1] += p.y;
+          v[2] += p.z;
+          v[3] += p.w;
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) own[k][j] = (r + j < r_a) ? v[j] * pre : 0.0f;
+      const int row = rank * kTcOwn + ml;
+      if (a.t && row < tile.rows && r < a.R)
+        *reinterpret_cast<float4 *>(a.t + (int64_t)(tile.row0 + row) * a.R + r) =
+            make_float4(own[k][0], own[k][1], own[k][2], own[k][3]);
+    }
+    __syncwarp();
+    if (lane < kTcCS) mbar_arrive_cta(B.taken, lane);  // this CTA's buffer may be overwritten by t
+    ok = vote(mbar_wait_cluster(B.taken, 0));
+  }
+  if (ok) {
+    const float post = (UP == 0) ? a.scales[tile.adapter] : 1.0f;  // to what the up step multiplies
+#pragma unroll
+    for (int k = 0; k < G::PER_THREAD; ++k) {
+      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * kTcOwn + ml;
+      float2 sc = make_float2(1.0f, 1.0f);
+      if (XT == 0) {
+        float mx = fmaxf(fmaxf(fabsf(own[k][0] * post), fabsf(own[k][1] * post)),
+                         fmaxf(fabsf(own[k][2] * post), fabsf(own[k][3] * post)));
+#pragma unroll
+        for (int o = 1; o < RP / 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        sc = tc_scale(mx);
+      }
+      uint2 hi, lo;
+      tc_split<XT>(own[k][0] * post * sc.y, own[k][1] * post * sc.y, hi.x, lo.x);
+      tc_split<XT>(own[k][2] * post * sc.y, own[k][3] * post * sc.y, hi.y, lo.y);
+      const int at = (r >> 6) * (kTcRows * 128) + row * 128 + ((((r & 63) >> 3) ^ (row & 7)) << 4) + (r & 7) * 2;
+      for (int q = 0; q < kTcCS; ++q) {
+        unsigned char *to = cluster.map_shared_rank(smem, q);
+        if (r < r16) {
+          *reinterpret_cast<uint2 *>(to + NS * G::SLOT + at) = hi;
+          *reinterpret_cast<uint2 *>(to + NS * G::SLOT + G::BLOCKS * kTcRows * 128 + at) = lo;
+        }
+        if (XT == 0 && r == 0) *reinterpret_cast<float *>(to + G::scale_off + 4 * row) = sc.x;
+      }
+    }
+    fence_proxy_async_all();  // t is read by the tensor cores
+    __syncwarp();
+    if (lane < kTcCS) mbar_arrive_cta(B.t_in, lane);
+    ok = vote(mbar_wait_cluster(B.t_in, 0));
+    fence_proxy_async_all();
+    __syncwarp();
+    if (ok && lane == 0) mbar_arrive(B.t_ready);
+  }
+
+  // ---- up: base + t W2, 64 columns a step, 32 per half ------------------------
+  const float row_scale = (XT == 0 && ok) ? *reinterpret_cast<const float *>(smem + G::scale_off + 4 * m) : 1.0f;
+  for (int j = 0; j < U && ok; ++j) {
+    const int s = D + j, slot = s % NS, buf = j & 1;
+    const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES;
+    ok = vote(!*abort && mbar_wait(B.full + 8u * slot, (s / NS) & 1));
+    if (!ok) break;
+    if (patch) {
+      if (pad && UP == 0 && wt < 128) {  // W2 [64 rows][ranks]: zero ranks r_a .. r16 - 1
+        const int n = wt >> 1, r = r16 - 16 + 8 * (wt & 1), left = r_a - r;
+        if (left < 8) {
+          const uint32_t at = ws + (r >> 6) * 8192 + n * 128 + ((((r & 63) >> 3) ^ (n & 7)) << 4);
+          const uint4 v = lds_v4(at);
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] &= (left > 2 * k + 1) ? 0xffffffffu : (left > 2 * k) ? 0x0000ffffu : 0u;
+          sts_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
+      if (pad && UP == 1 && wt < 8 * (r16 - r_a)) sts_v4(ws + (r_a + (wt >> 3)) * 128 + (wt & 7) * 16, make_uint4(0, 0, 0, 0));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.masked + 8u * slot);
+    }
+    ok = vote(mbar_wait(B.d_full + 8u * buf, (j >> 1) & 1));
+    if (!ok) break;
+    tc_fence_after();
+    uint32_t d[32];
+    tmem_ld32(tmem + lane_addr + RP + 64 * buf + 32 * half, d);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.d_empty + 8u * buf);
+    const int col0 = o_begin + 64 * j;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = 4 * half + q;
+      const uint32_t at = xs + m * 128 + ((c ^ (m & 7)) << 4);
+      uint4 b = make_uint4(0, 0, 0, 0);
+      if (a.base) b = lds_v4(at);
+      uint4 keep = make_uint4(0, 0, 0, 0);
+      if (UP == 1 && drop) keep = drop_block(dst, (uint32_t)(col0 >> 3) + c, (uint32_t)(tile.row0 + m));
+      const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+      uint32_t ow[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v0 = __uint_as_float(d[8 * q + 2 * i]), v1 = __uint_as_float(d[8 * q + 2 * i + 1]);
+        if (XT == 0) {
+          v0 *= row_scale;
+          v1 *= row_scale;
+        }
+        if (UP == 1 && drop) {
+          v0 = drop_keep(keep, 2 * i, dst.thr_hi) ? v0 * a.drop.inv_keep : 0.0f;
+          v1 = drop_keep(keep, 2 * i + 1, dst.thr_hi) ? v1 * a.drop.inv_keep : 0.0f;
+        }
+        const float2 bf = Elem<XT>::pair(bw[i]);
+        ow[i] = (uint32_t)Elem<XT>::from_float(bf.x + v0) | ((uint32_t)Elem<XT>::from_float(bf.y + v1) << 16);
+      }
+      sts_v4(at, make_uint4(ow[0], ow[1], ow[2], ow[3]));
+    }
+    __syncwarp();
+    // this warp's 32 rows x 64 bytes leave in whole sectors
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int row = quad * 32 + it * 8 + (lane >> 2), c = 4 * half + (lane & 3), col = col0 + 8 * c;
+      if (row < tile.rows && col < o_end)
+        st_v4(a.y + (tile.row0 + row) * a.ldy + col, lds_v4(xs + row * 128 + ((c ^ (row & 7)) << 4)));
+    }
+    fence_proxy_async_smem();  // the slot's next contents come by TMA
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.free_out + 8u * slot);
+  }
+  if (!ok && lane == 0) {
+    if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+    *abort = 1;
+  }
+}
+
+// grid = 8 x tiles, cluster = (8, 1, 1).  mx: x [M, Ci]; mA: A {K, R, L}, boxes
+// of 64 columns x 16 ranks; mB: B {R, N, L}, boxes of 64 ranks x 64 rows;
+// mbase: base [M, Co].
+template <int XT, int UP, int RP>
+__global__ void __launch_bounds__(kTcThreads, RP == 64 ? 2 : 1)
+lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mA,
+               const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mbase, const LoraArgs a) {
+  using G = TcGeom<RP>;
+  constexpr int NS = G::NS;
+  extern __shared__ __align__(1024) unsigned char tsm_raw[];
+  const uint32_t raw = smem_u32(tsm_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char *smem = tsm_raw + (sbase - raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % kTcCS, tile_index = (int)blockIdx.x / kTcCS;
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
+  const TcBars B(sbase + G::bar_off, NS);
+
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x == 0 && warp == kTcWorkers + 1)
+    lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
+  const LoraTile tile = lora_find_tile<kTcRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
+  if (!tile.found) return;  // the whole cluster
+  const int r_a = lora_rank(a.ranks, tile.adapter, a.L, a.R);
+  const int o_begin = rank * a.slice_o, o_end = min(a.Co, o_begin + a.slice_o);
+  if (r_a == 0) {
+    lora_copy_rows(a, tile, o_begin, o_end, rank == 0, kTcThreads);
+    return;
+  }
+  const int r16 = (r_a + 15) & ~15;
+  const int c_begin = rank * a.slice_c, c_end = min(a.Ci, c_begin + a.slice_c);
+  const int D = c_end > c_begin ? (c_end - c_begin + 63) / 64 : 0;  // steps down
+  const int U = o_end > o_begin ? (o_end - o_begin + 63) / 64 : 0;  // steps up
+  const bool drop = a.drop.thr != 0;
+  const bool pad = (r_a & 15) != 0;                 // the last k-step of the up product needs zeros
+  const bool patch = pad || (UP == 0 && drop);     // workers touch the slots before the MMA
+  const int blocks = (r_a + 63) / 64;              // 64-rank blocks in use
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(B.full + 8u * i, 1);
+      mbar_init(B.masked + 8u * i, kTcWorkers);
+      mbar_init(B.free_mma + 8u * i, 1);
+      mbar_init(B.free_out + 8u * i, kTcWorkers);
+    }
+    mbar_init(B.p_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.d_full + 8u * i, 1);
+      mbar_init(B.d_empty + 8u * i, kTcWorkers);
+    }
+    mbar_init(B.recv, kTcCS * kTcWorkers);
+    mbar_init(B.taken, kTcCS * kTcWorkers);
+    mbar_init(B.t_in, kTcCS * kTcWorkers);
+    mbar_init(B.t_ready, kTcWorkers);
+    mbar_init(B.done, 1);
+    *abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + G::tmem_off),
+                 "n"(G::TM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();  // barriers are initialised in every CTA before any remote arrival
+  cluster_wait();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + G::tmem_off);
+  const uint32_t t_smem = sbase + NS * G::SLOT;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int boxes = (tile.rows + kTcXBox - 1) / kTcXBox;
+      int s = 0;
+      for (; s < D + U; ++s) {
+        const int slot = s % NS, prev = s - NS;
+        if (prev >= 0) {
+          // the slot's last use: a step down is freed by its MMAs, a step up by the workers
+          const int first_up = D + (slot - D % NS + NS) % NS;  // first step up in this slot
+          const uint32_t bar = prev < D ? B.free_mma + 8u * slot : B.free_out + 8u * slot;
+          const int use = prev < D ? prev / NS : (prev - first_up) / NS;
+          if (*abort || !mbar_wait(bar, use & 1)) {
+            if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+            *abort = 1;
+            break;
+          }
+        }
+        const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES, full = B.full + 8u * slot;
+        const bool down = s < D;
+        const int c = down ? c_begin + 64 * s : o_begin + 64 * (s - D);
+        const bool from_a = down == (UP == 0);   // this step reads A (16-rank boxes), else B
+        const bool rows_in = down || a.base;
+        mbar_arrive_expect_tx(full, (rows_in ? boxes * kTcXBox * 128 : 0) + (from_a ? r16 * 128 : blocks * 8192));
+        if (rows_in)
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(xs + i * kTcXBox * 128, down ? &mx : &mbase, c, tile.row0 + i * kTcXBox, full);
+        if (from_a)
+          for (int i = 0; i < r16 / 16; ++i) tma_load_3d(ws + i * 2048, &mA, c, i * 16, tile.adapter, full);
+        else
+          for (int i = 0; i < blocks; ++i) tma_load_3d(ws + i * 8192, &mB, i * 64, c, tile.adapter, full);
+      }
+      // every copy has landed before the CTA may exit
+      for (int j = 1; j <= NS && j <= s; ++j) mbar_wait(B.full + 8u * ((s - j) % NS), ((s - j) / NS) & 1, 1u << 20);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t ready = patch ? B.masked : B.full;
+      bool ok = true;
+      // down: P [128 rows, r16] = x . W1, A operand x (K-major); W1 = A [r][64 c]
+      // (K-major) forward, B [64 c][r] (MN-major) in the gradient
+      const uint32_t id_down = tc_idesc<XT>(r16, false, UP == 1);
+      for (int s = 0; s < D && ok; ++s) {
+        const int slot = s % NS;
+        ok = !*abort && mbar_wait(ready + 8u * slot, (s / NS) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma(tmem, tc_desc(xs + 32 * k, 16), UP == 0 ? tc_desc(ws + 32 * k, 16) : tc_desc(ws + 2048 * k, 8192), id_down,
+                 s > 0 || k > 0);
+        umma_commit(B.free_mma + 8u * slot);
+      }
+      if (ok && D > 0) umma_commit(B.p_full);
+      // up: 64 output columns a step, A operand t (hi, then lo); W2 = B [64 c][r]
+      // (K-major) forward, A [r][64 c] (MN-major) in the gradient
+      const uint32_t id_up = tc_idesc<XT>(64, false, UP == 1);
+      if (ok && U > 0) ok = mbar_wait(B.t_ready, 0);
+      for (int j = 0; j < U && ok; ++j) {
+        const int s = D + j, slot = s % NS, buf = j & 1;
+        ok = !*abort && mbar_wait(ready + 8u * slot, (s / NS) & 1) &&
+             (j < 2 || mbar_wait(B.d_empty + 8u * buf, ((j >> 1) & 1) ^ 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ws = sbase + slot * G::SLOT + G::X_BYTES;
+        for (int part = 0; part < 2; ++part)
+          for (int k = 0; k < r16 / 16; ++k) {
+            const uint32_t ta = t_smem + (part * G::BLOCKS + k / 4) * (kTcRows * 128) + 32 * (k % 4);
+            const uint64_t wd = UP == 0 ? tc_desc(ws + (k / 4) * 8192 + 32 * (k % 4), 16) : tc_desc(ws + 2048 * k, 8192);
+            tc_mma(tmem + RP + 64 * buf, tc_desc(ta, 16), wd, id_up, part > 0 || k > 0);
+          }
+        umma_commit(B.d_full + 8u * buf);
+      }
+      if (!ok) {
+        if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+        *abort = 1;
+      }
+    }
+    __syncwarp();
+  } else {
+    lora_tc_workers<XT, UP, RP>(a, tile, r_a, r16, D, U, patch, pad, o_begin, o_end, c_begin, rank, tmem, sbase, smem, B,
+                                abort, cluster);
+  }
+
+  // everything issued by this CTA has finished before the tensor memory goes
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (*abort && lane == 0) {
+      umma_commit(B.done);
+      mbar_wait(B.done, 0, 1u << 20);
+    }
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(G::TM_COLS) : "memory");
+  }
+  cluster_arrive();  // no CTA leaves while another may still write into its shared memory
+  cluster_wait();
+}
+
+// ---------------------------------------------------------------------------
+// weight gradients
+// ---------------------------------------------------------------------------
+//   dA[a] = sum_m dt[m]^T drop(x)[m]        [R, K]
+//   dB[a] = sum_m s_a dy[m]^T t[m]          [N, R]
+// Both are G[c, r] = sum_m X[m, c] P[m, r] over the rows of the adapter's
+// segments, X 16-bit and P fp32: tcgen05.mma with the column c as M = 128 and
+// the rank as N, both operands MN-major (their rows run along the
+// contraction, as they lie in memory).  One launch does both gradients: a
+// cluster of 8 CTAs owns 128 columns of one adapter's dA or dB, its CTAs take
+// the adapter's 64-row tiles in turn, and their fp32 sums meet in distributed
+// shared memory in rank order: no atomics, no partial gradients in global
+// memory, and an adapter that occurs in several segments is summed by one
+// cluster.
+// P enters as 16-bit parts side by side along N, so that one matrix
+// instruction multiplies all of them: bf16 three parts (24 bits); fp16 two,
+// P scaled by a power of two that brings the largest of the CTA's rows into
+// [2^14, 2^15).  X is read once; P once for each 128 columns (from L2).
+
+struct WgradSide {
+  const float *P;     // [M, R]
+  float *out;         // dA [L, R, C], or dB [L, C, R]
+  int C;
+  int tiles;          // column tiles; 0 if this gradient is not wanted
+};
+
+struct WgradArgs {
+  WgradSide dA, dB;
+  const int *ranks;
+  const float *scales;
+  const int *seg_off, *seg_adapter;
+  int64_t M;
+  int R, L, S;
+  DropArgs drop;  // on dA's X
+};
+
+constexpr int kWgRows = 64;   // rows per step
+constexpr int kWgCols = 128;  // columns per cluster (MMA M)
+
+template <int RP> struct WgradGeom {
+  static constexpr int X_BYTES = kWgRows * kWgCols * 2;
+  static constexpr int PB = 3 * RP / 64;                 // 64-wide blocks of P's parts
+  static constexpr int P_BYTES = PB * kWgRows * 128;
+  static constexpr int XS = (RP == 64) ? 3 : 4, PS = 2;  // stages
+  static constexpr int RING = XS * X_BYTES + PS * P_BYTES;
+  static constexpr int RECV = kWgCols * RP * 4;
+  static_assert(RECV <= RING, "the sums' buffer lies over the ring");
+  static constexpr int bar_off = RING;
+  static constexpr int nbar = 2 * XS + 2 * PS + 2;
+  static constexpr int max_off = bar_off + 8 * nbar;     // largest |P| (fp16), as bits
+  static constexpr int tmem_off = max_off + 4;
+  static constexpr int abort_off = tmem_off + 4;
+  static constexpr int total = abort_off + 4 + 1024;
+  static constexpr int TM_COLS = (RP == 64) ? 256 : 512;
+  static constexpr int PPT = kWgRows * RP / 4 / (32 * kTcWorkers);  // quads of P per worker
+};
+
+// The 64-row tiles of one adapter, in order: every warp walks all of them and
+// takes those whose number is its CTA's rank modulo 8.
+struct WgradRows {
+  int s0;            // first segment not looked at
+  unsigned mask;     // segments of the last 32 that are left
+  int start, len;    // this lane's segment
+  int cur, cur_len;  // segment being cut: next row, rows left
+  int count;         // tiles passed
+  int row0, rows;    // the tile found
+};
+
+BQ_DEV bool wgrad_next(WgradRows &w, const WgradArgs &a, int adapter, int rank) {
+  const int lane = threadIdx.x & 31;
+  while (true) {
+    while (w.cur_len <= 0) {
+      while (!w.mask) {
+        if (w.s0 >= a.S) return false;
+        const int s = w.s0 + lane;
+        bool hit = false;
+        w.len = 0;
+        if (s < a.S && a.seg_adapter[s] == adapter) {
+          w.len = lora_segment(a.seg_off, s, a.M, &w.start);
+          hit = w.len > 0;
+        }
+        w.mask = __ballot_sync(0xffffffffu, hit);
+        w.s0 += 32;
+      }
+      const int src = __ffs(w.mask) - 1;
+      w.mask &= w.mask - 1;
+      w.cur = __shfl_sync(0xffffffffu, w.start, src);
+      w.cur_len = __shfl_sync(0xffffffffu, w.len, src);
+    }
+    // tiles count .. count + n - 1 are this segment's; skip to this CTA's
+    const int skip = (rank - w.count) & (kTcCS - 1);
+    const int n = (w.cur_len + kWgRows - 1) / kWgRows;
+    if (skip >= n) {
+      w.count += n;
+      w.cur_len = 0;
+      continue;
+    }
+    w.row0 = w.cur + skip * kWgRows;
+    w.rows = min(kWgRows, w.cur_len - skip * kWgRows);
+    w.count += skip + 1;
+    w.cur += (skip + 1) * kWgRows;
+    w.cur_len -= (skip + 1) * kWgRows;
+    return true;
+  }
+}
+
+struct WgradBars {
+  uint32_t full, freed, ready, p_free, d_full, done;
+  BQ_DEV WgradBars(uint32_t base, int xs, int ps) {
+    full = base;                 // [XS] X has landed
+    freed = full + 8u * xs;      // [XS] its MMAs are done
+    ready = freed + 8u * xs;     // [PS] P is stored (and X patched)
+    p_free = ready + 8u * ps;    // [PS] its MMAs are done
+    d_full = p_free + 8u * ps;
+    done = d_full + 8u;
+  }
+};
+
+// P's quad v as parts at (row m, rank r) of a stage.
+template <int XT> BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r16, float4 v) {
+  uint2 part[3];
+  if (XT == 1) {
+    float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      part[p].x = pack_bf16(f[0], f[1]);
+      part[p].y = pack_bf16(f[2], f[3]);
+      f[0] -= __uint_as_float(part[p].x << 16);
+      f[1] -= __uint_as_float(part[p].x & 0xffff0000u);
+      f[2] -= __uint_as_float(part[p].y << 16);
+      f[3] -= __uint_as_float(part[p].y & 0xffff0000u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(fabsf(f[i]) <= 3.402823466e38f)) f[i] = 0.0f;  // infinite or NaN: the first part says it
+    }
+  } else {
+    tc_split<0>(v.x, v.y, part[0].x, part[1].x);
+    tc_split<0>(v.z, v.w, part[0].y, part[1].y);
+  }
+#pragma unroll
+  for (int p = 0; p < (XT == 1 ? 3 : 2); ++p) {
+    const int n = p * r16 + r;
+    const uint32_t at = stage + (n >> 6) * (kWgRows * 128) + m * 128 + ((((n & 63) >> 3) ^ (m & 7)) << 4) + (n & 7) * 2;
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(part[p].x), "r"(part[p].y) : "memory");
+  }
+}
+
+// grid = 8 x (L x (dA tiles + dB tiles)), cluster = (8, 1, 1); mx: x [M, K],
+// mdy: dy [M, N], boxes of 64 columns x 16 rows.
+template <int XT, int RP>
+__global__ void __launch_bounds__(kTcThreads, RP == 64 ? 2 : 1)
+lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mdy, const WgradArgs a) {
+  using G = WgradGeom<RP>;
+  constexpr int XS = G::XS, PS = G::PS, PARTS = XT == 1 ? 3 : 2;
+  extern __shared__ __align__(1024) unsigned char tsm_raw[];
+  const uint32_t raw = smem_u32(tsm_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char *smem = tsm_raw + (sbase - raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x % kTcCS, work = (int)blockIdx.x / kTcCS;
+  const int per_adapter = a.dA.tiles + a.dB.tiles, adapter = work / per_adapter;
+  const bool is_b = work % per_adapter >= a.dA.tiles;
+  const WgradSide side = is_b ? a.dB : a.dA;
+  const CUtensorMap *map = is_b ? &mdy : &mx;
+  const int c0 = (work % per_adapter - (is_b ? a.dA.tiles : 0)) * kWgCols;
+  const int r_a = lora_rank(a.ranks, adapter, a.L, a.R), r16 = (r_a + 15) & ~15;
+  const int nfull = PARTS * r16, n0 = nfull < 192 ? nfull : 192, n1 = nfull - n0;  // columns of the two MMAs
+  const int cblocks = side.C - c0 > 64 ? 2 : 1;
+  const bool masked = !is_b && a.drop.thr != 0;
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
+  const WgradBars B(sbase + G::bar_off, XS, PS);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < XS; ++i) {
+      mbar_init(B.full + 8u * i, 1);
+      mbar_init(B.freed + 8u * i, 1);
+    }
+    for (int i = 0; i < PS; ++i) {
+      mbar_init(B.ready + 8u * i, kTcWorkers);
+      mbar_init(B.p_free + 8u * i, 1);
+    }
+    mbar_init(B.d_full, 1);
+    mbar_init(B.done, 1);
+    *abort = 0;
+    *reinterpret_cast<volatile uint32_t *>(smem + G::max_off) = 0u;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + G::tmem_off),
+                 "n"(G::TM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + G::tmem_off);
+
+  WgradRows w = {};
+  int steps = 0;  // tiles taken
+  float2 pscale = make_float2(1.0f, 1.0f);
+  if (r_a == 0) {
+    // no rank: nothing to sum
+  } else if (warp == 0) {
+    while (wgrad_next(w, a, adapter, rank)) {
+      const int slot = steps % XS;
+      bool ok = true;
+      if (steps >= XS) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.freed + 8u * slot, ((steps / XS) & 1) ^ 1)) != 0;
+      if (!ok) {
+        if (lane == 0) {
+          if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+          *abort = 1;
+        }
+        break;
+      }
+      if (lane == 0) {
+        const uint32_t xs = sbase + slot * G::X_BYTES, full = B.full + 8u * slot;
+        const int boxes = (w.rows + kTcWXBox - 1) / kTcWXBox;
+        mbar_arrive_expect_tx(full, cblocks * boxes * kTcWXBox * 128);
+        for (int b = 0; b < cblocks; ++b)
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(xs + b * (kWgRows * 128) + i * kTcWXBox * 128, map, c0 + 64 * b, w.row0 + i * kTcWXBox, full);
+      }
+      __syncwarp();
+      ++steps;
+    }
+    // every copy has landed before the ring is used for the sums
+    for (int j = 1; j <= XS && j <= steps; ++j)
+      mbar_wait(B.full + 8u * ((steps - j) % XS), ((steps - j) / XS) & 1, 1u << 20);
+  } else if (warp == 1) {
+    bool ok = true;
+    const uint32_t id0 = tc_idesc<XT>(n0, true, true), id1 = tc_idesc<XT>(n1 > 0 ? n1 : 16, true, true);
+    while (wgrad_next(w, a, adapter, rank)) {
+      const int slot = steps % XS, ps = steps % PS;
+      ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.full + 8u * slot, (steps / XS) & 1) &&
+                                       mbar_wait(B.ready + 8u * ps, (steps / PS) & 1)) != 0;
+      if (!ok) break;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + ps * G::P_BYTES;
+        const int ks = (w.rows + 15) / 16;
+        for (int k = 0; k < ks; ++k) {
+          const uint64_t xd = tc_desc(xb + 2048 * k, kWgRows * 128);
+          tc_mma(tmem, xd, tc_desc(pb + 2048 * k, kWgRows * 128), id0, steps > 0 || k > 0);
+          if (n1 > 0)
+            tc_mma(tmem + n0, xd, tc_desc(pb + 3 * (kWgRows * 128) + 2048 * k, kWgRows * 128), id1, steps > 0 || k > 0);
+        }
+        umma_commit(B.freed + 8u * slot);
+        umma_commit(B.p_free + 8u * ps);
+      }
+      __syncwarp();
+      ++steps;
+    }
+    if (lane == 0) {
+      if (ok) umma_commit(B.d_full);
+      else {
+        if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+        *abort = 1;
+      }
+    }
+    __syncwarp();
+  } else {
+    const int wt = (int)threadIdx.x - 64;
+    const DropState dst = drop_state(a.drop);
+    bool ok = true;
+    auto load_p = [&](float4 (&pv)[G::PPT], int row0, int rows) {
+#pragma unroll
+      for (int k = 0; k < G::PPT; ++k) {
+        const int i = wt + k * 32 * kTcWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
+        pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (m < rows && r < r_a) {
+          pv[k] = *reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r);
+          if (r + 1 >= r_a) pv[k].y = 0.0f;
+          if (r + 2 >= r_a) pv[k].z = 0.0f;
+          if (r + 3 >= r_a) pv[k].w = 0.0f;
+        }
+      }
+    };
+    if (XT == 0) {  // the power of two that brings the largest |P| of these rows below fp16's range
+      WgradRows v = {};
+      float mx = 0.0f;
+      while (wgrad_next(v, a, adapter, rank)) {
+        float4 pv[G::PPT];
+        load_p(pv, v.row0, v.rows);
+#pragma unroll
+        for (int k = 0; k < G::PPT; ++k) {
+          const float q[4] = {fabsf(pv[k].x), fabsf(pv[k].y), fabsf(pv[k].z), fabsf(pv[k].w)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (q[i] <= 3.402823466e38f) mx = fmaxf(mx, q[i]);  // infinite and NaN stay what they are
+        }
+      }
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      if (lane == 0) atomicMax(reinterpret_cast<unsigned *>(smem + G::max_off), __float_as_uint(mx));
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kTcWorkers) : "memory");
+      pscale = tc_scale(__uint_as_float(*reinterpret_cast<volatile uint32_t *>(smem + G::max_off)));
+    }
+    float4 pv[G::PPT];
+    bool more = wgrad_next(w, a, adapter, rank);
+    if (more) load_p(pv, w.row0, w.rows);
+    while (more) {
+      const int slot = steps % XS, ps = steps % PS, row0 = w.row0, rows = w.rows;
+      const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + ps * G::P_BYTES;
+      if (steps >= PS) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.p_free + 8u * ps, ((steps / PS) & 1) ^ 1)) != 0;
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < G::PPT; ++k) {
+        const int i = wt + k * 32 * kTcWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
+        float4 v = pv[k];
+        if (XT == 0) v = make_float4(v.x * pscale.y, v.y * pscale.y, v.z * pscale.y, v.w * pscale.y);
+        if (r < r16) wgrad_store_p<XT>(pb, m, r, r16, v);
+      }
+      more = wgrad_next(w, a, adapter, rank);
+      if (more) load_p(pv, w.row0, w.rows);
+      const int rows16 = (rows + 15) & ~15;
+      if (masked || rows16 != rows) {
+        ok = __all_sync(0xffffffffu, mbar_wait(B.full + 8u * slot, (steps / XS) & 1)) != 0;
+        if (!ok) break;
+        for (int i = wt; i < cblocks * rows16 * 8; i += 32 * kTcWorkers) {
+          const int c = i & 7, m = (i >> 3) % rows16, b = (i >> 3) / rows16;
+          const uint32_t at = xb + b * (kWgRows * 128) + m * 128 + ((c ^ (m & 7)) << 4);
+          if (m >= rows) {
+            sts_v4(at, make_uint4(0, 0, 0, 0));  // another segment's row
+          } else if (masked) {
+            const uint4 g = drop_mask8(drop_block(dst, (uint32_t)(c0 >> 3) + 8 * b + c, (uint32_t)(row0 + m)), dst.thr_hi);
+            uint4 v = lds_v4(at);
+            v.x &= g.x;
+            v.y &= g.y;
+            v.z &= g.z;
+            v.w &= g.w;
+            sts_v4(at, v);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.ready + 8u * ps);
+      ++steps;
+    }
+    if (ok) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.d_full, 0)) != 0;
+    if (!ok && lane == 0) {
+      if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+      *abort = 1;
+    }
+  }
+
+  // ---- the sums meet: every CTA's ring is idle, it holds the sums now --------
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    if (*abort && lane == 0) {
+      umma_commit(B.done);
+      mbar_wait(B.done, 0, 1u << 20);
+    }
+    __syncwarp();
+  }
+  cluster_arrive();
+  cluster_wait();
+  float *recv = reinterpret_cast<float *>(smem);
+  const int per_r = r16 / kTcCS;  // ranks of dA that one CTA owns (dB: 16 columns)
+  if (warp >= 2 && r_a > 0) {
+    const int quad = warp & 3, half = (warp - 2) >> 2, c = quad * 32 + lane;
+    const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
+    for (int cgp = half; cgp < r16 / 16; cgp += 2) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      if (steps > 0) {
+#pragma unroll
+        for (int p = PARTS - 1; p >= 0; --p) {  // the smallest part first
+          float q[16];
+          tmem_ld16(at + p * r16 + cgp * 16, q);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += q[i];
+        }
+      }
+      if (XT == 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= pscale.x;
+      }
+      if (!is_b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = cgp * 16 + i;
+          cluster.map_shared_rank(recv, r / per_r)[(rank * per_r + r % per_r) * kWgCols + c] = v[i];
+        }
+      } else {
+        float *to = cluster.map_shared_rank(recv, c / kTcOwn) + (rank * kTcOwn + c % kTcOwn) * RP;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4 *>(to + 4 * ((cgp * 4 + q) ^ (c & 7))) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(G::TM_COLS) : "memory");
+  }
+  const float scale = is_b ? (r_a > 0 ? a.scales[adapter] : 0.0f) : (masked ? a.drop.inv_keep : 1.0f);
+  auto finish = [&](float4 v) {  // an unused adapter's gradient is 0 whatever its scale
+    return make_float4(v.x != 0.0f ? v.x * scale : 0.0f, v.y != 0.0f ? v.y * scale : 0.0f,
+                       v.z != 0.0f ? v.z * scale : 0.0f, v.w != 0.0f ? v.w * scale : 0.0f);
+  };
+  if (!is_b) {
+    // this CTA's ranks (and, behind r16, every eighth zero row), 128 columns each
+    const int zero_rows = a.R > r16 ? (a.R - r16 - rank + kTcCS - 1) / kTcCS : 0;
+    for (int i = threadIdx.x; i < (per_r + zero_rows) * (kWgCols / 4); i += kTcThreads) {
+      const int rl = i / (kWgCols / 4), c = 4 * (i % (kWgCols / 4));
+      const int r = rl < per_r ? rank * per_r + rl : r16 + rank + (rl - per_r) * kTcCS;
+      if (r >= a.R || c0 + c >= side.C) continue;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (r < r_a) {
+        for (int q = 0; q < kTcCS; ++q) {
+          const float4 p = *reinterpret_cast<const float4 *>(recv + (q * per_r + rl) * kWgCols + c);
+          v.x += p.x;
+          v.y += p.y;
+          v.z += p.z;
+          v.w += p.w;
+        }
+        v = finish(v);
+      }
+      *reinterpret_cast<float4 *>(side.out + ((int64_t)adapter * a.R + r) * side.C + c0 + c) = v;
+    }
+  } else {
+    const int quads = a.R / 4;
+    for (int i = threadIdx.x; i < kTcOwn * quads; i += kTcThreads) {
+      const int cl = i / quads, chunk = i % quads, c = c0 + rank * kTcOwn + cl;
+      if (c >= side.C) continue;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (4 * chunk < r_a) {
+        for (int q = 0; q < kTcCS; ++q) {
+          const float4 p = *reinterpret_cast<const float4 *>(recv + (q * kTcOwn + cl) * RP + 4 * (chunk ^ (cl & 7)));
+          v.x += p.x;
+          v.y += p.y;
+          v.z += p.z;
+          v.w += p.w;
+        }
+        v = finish(v);
+        if (4 * chunk + 1 >= r_a) v.y = 0.0f;
+        if (4 * chunk + 2 >= r_a) v.z = 0.0f;
+        if (4 * chunk + 3 >= r_a) v.w = 0.0f;
+      }
+      *reinterpret_cast<float4 *>(side.out + ((int64_t)adapter * side.C + c) * a.R + 4 * chunk) = v;
+    }
+  }
+}
+
+}  // namespace bq
