@@ -958,21 +958,21 @@ bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
 }
 
 // Long segments: 128-row tiles on tcgen05.
-template <int XT, int UP, int RP>
+template <int XT, int UP, int RP, int CS>
 bq_status launch_lora_tc(LoraArgs a, cudaStream_t st) {
-  using G = TcGeom<RP>;
+  using G = TcGeom<RP, CS>;
   CUtensorMap mx = {}, mA = {}, mB = {}, mbase = {};
   const int64_t K = UP ? a.Co : a.Ci, N = UP ? a.Ci : a.Co;
   if (!make_map(&mx, a.x, XT == 1, a.Ci, a.M, 0, a.ldx, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
   if (K && !make_map(&mA, a.A, XT == 1, K, a.R, a.L, K, (int64_t)a.R * K, 64, 16)) return BQ_ERR_CUDA;
   if (N && !make_map(&mB, a.B, XT == 1, a.R, N, a.L, a.R, (int64_t)a.R * N, 64, 64)) return BQ_ERR_CUDA;
   if (a.base && a.Co && !make_map(&mbase, a.base, XT == 1, a.Co, a.M, 0, a.ldbase, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
-  a.CS = kTcCS;
-  a.slice_c = (int)round_up((a.Ci + kTcCS - 1) / kTcCS, 64);
-  a.slice_o = (int)round_up((a.Co + kTcCS - 1) / kTcCS, 64);
-  constexpr auto kern = lora_tc_kernel<XT, UP, RP>;
+  a.CS = CS;
+  a.slice_c = (int)round_up((a.Ci + CS - 1) / CS, 64);
+  a.slice_o = (int)round_up((a.Co + CS - 1) / CS, 64);
+  constexpr auto kern = lora_tc_kernel<XT, UP, RP, CS>;
   if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
-  return launch_cluster(kern, lora_tiles(a, kTcRows) * kTcCS, kTcCS, kTcThreads, G::total, overlap_mode() >= 1, st, mx,
+  return launch_cluster(kern, lora_tiles(a, kTcRows) * CS, CS, kTcThreads, G::total, overlap_mode() >= 1, st, mx,
                         mA, mB, mbase, a);
 }
 
@@ -984,7 +984,10 @@ bq_status launch_lora(const LoraArgs &a, cudaStream_t st) {
     if (a.R <= 16) return launch_lora_t<XT, UP, 16>(a, st);
     return a.R <= 64 ? launch_lora_t<XT, UP, 64>(a, st) : launch_lora_t<XT, UP, 128>(a, st);
   }
-  return a.R <= 64 ? launch_lora_tc<XT, UP, 64>(a, st) : launch_lora_tc<XT, UP, 128>(a, st);
+  // clusters of 8 as long as they fit the GPU at once, else of 4
+  const bool wide = lora_tiles(a, kTcRows) * 8 <= (a.R <= 64 ? 2 : 1) * (int64_t)sm_count();
+  if (a.R <= 64) return wide ? launch_lora_tc<XT, UP, 64, 8>(a, st) : launch_lora_tc<XT, UP, 64, 4>(a, st);
+  return wide ? launch_lora_tc<XT, UP, 128, 8>(a, st) : launch_lora_tc<XT, UP, 128, 4>(a, st);
 }
 
 struct WgradInputs {
@@ -996,15 +999,20 @@ template <int XT, int RP>
 bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, cudaStream_t st) {
   using G = WgradGeom<RP>;
   CUtensorMap mx = {}, mdy = {};
-  if (a.dA.out) a.dA.tiles = (a.dA.C + kWgCols - 1) / kWgCols;
-  if (a.dB.out) a.dB.tiles = (a.dB.C + kWgCols - 1) / kWgCols;
+  if (a.dA.out) a.dA.tiles = (a.dA.C + G::CT - 1) / G::CT;
+  if (a.dB.out) a.dB.tiles = (a.dB.C + G::CT - 1) / G::CT;
   const int64_t clusters = (int64_t)a.L * (a.dA.tiles + a.dB.tiles);
   if (clusters == 0) return BQ_OK;
   if (a.S && a.dA.tiles && !make_map(&mx, in.x, XT == 1, a.dA.C, a.M, 0, in.ldx, 0, 64, kTcWXBox)) return BQ_ERR_CUDA;
   if (a.S && a.dB.tiles && !make_map(&mdy, in.dy, XT == 1, a.dB.C, a.M, 0, in.lddy, 0, 64, kTcWXBox)) return BQ_ERR_CUDA;
   constexpr auto kern = lora_wgrad_kernel<XT, RP>;
   if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
-  return launch_cluster(kern, clusters * kTcCS, kTcCS, kTcThreads, G::total, false, st, mx, mdy, a);
+  // CTAs per cluster: enough to fill the GPU with the adapters that can be in
+  // use; more than that only shortens each CTA's run of rows
+  const int64_t busy = (int64_t)(a.S < a.L ? a.S : a.L) * (a.dA.tiles + a.dB.tiles);
+  a.CS = 1;
+  while (a.CS < 8 && 2 * busy * a.CS <= (int64_t)sm_count()) a.CS *= 2;
+  return launch_cluster(kern, clusters * a.CS, a.CS, kTcThreads, G::total, false, st, mx, mdy, a);
 }
 
 // What bq_lora and bq_lora_grad have in common.

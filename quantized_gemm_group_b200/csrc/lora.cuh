@@ -125,18 +125,26 @@ BQ_DEV void lora_check_segments(const int *seg_off, const int *seg_adapter, cons
   if (bad) bq_flag(BQ_FLAG_BADMAP);
 }
 
-// Rows without a contribution: base's (nothing to do in place), t zero.
+// Rows without a contribution: base's (nothing to do in place), t zero.  A
+// warp takes a row at a time, eight loads in flight a lane.
 BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int o_begin, int o_end, bool with_t, int threads) {
-  const int per = (o_end - o_begin) / 8;  // 16-byte pieces of a row (may be <= 0)
+  const int lane = threadIdx.x & 31;
   if (a.base != a.y)
-    for (int64_t i = threadIdx.x; per > 0 && i < (int64_t)per * tile.rows; i += threads) {
-      const int m = (int)(i / per), c = o_begin + 8 * (int)(i - (int64_t)m * per);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (a.base) v = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m) * a.ldbase + c);
-      *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + c) = v;
+    for (int m = threadIdx.x >> 5; m < tile.rows; m += threads >> 5) {
+      const uint16_t *from = a.base + (tile.row0 + m) * a.ldbase;
+      uint16_t *to = a.y + (tile.row0 + m) * a.ldy;
+      for (int c = o_begin + 8 * lane; c < o_end; c += 8 * 256) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = (a.base && c + 256 * k < o_end) ? *reinterpret_cast<const uint4 *>(from + c + 256 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + 256 * k < o_end) st_v4(to + c + 256 * k, v[k]);
+      }
     }
   if (a.t && with_t)
-    for (int i = threadIdx.x; i < tile.rows * a.R; i += threads) a.t[(int64_t)tile.row0 * a.R + i] = 0.0f;
+    for (int64_t i = threadIdx.x; i < (int64_t)tile.rows * a.R; i += threads) a.t[(int64_t)tile.row0 * a.R + i] = 0.0f;
 }
 
 // The rank to use: 0 (no contribution) without an adapter or with a bad one.

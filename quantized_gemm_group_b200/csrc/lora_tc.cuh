@@ -39,9 +39,7 @@
 
 namespace bq {
 
-constexpr int kTcCS = 8;                       // CTAs per cluster
 constexpr int kTcRows = 128;                   // rows per tile (MMA M)
-constexpr int kTcOwn = kTcRows / kTcCS;        // rows whose sums one CTA owns
 constexpr int kTcWorkers = 8;                  // worker warps
 constexpr int kTcThreads = 32 * (2 + kTcWorkers);
 constexpr int kTcXBox = 32;                    // rows per TMA box of x and base
@@ -124,6 +122,13 @@ BQ_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Two floats rounded to a pair of type XT.
+template <int XT> BQ_DEV uint32_t pack_pair(float2 v) {
+  if (XT == 1) return pack_bf16(v.x, v.y);
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // Two floats as the hi and lo parts of type XT (fp16: scaled by the caller).
 template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t &lo) {
   if (XT == 1) {
@@ -152,7 +157,8 @@ BQ_DEV float2 tc_scale(float m) {
 // forward / input gradient
 // ---------------------------------------------------------------------------
 
-template <int RP> struct TcGeom {
+template <int RP, int CS> struct TcGeom {
+  static constexpr int OWN = kTcRows / CS;          // rows whose sums one CTA owns
   static constexpr int X_BYTES = kTcRows * 128;     // 128 rows x 64 columns
   static constexpr int W_BYTES = RP * 128;          // 64 x RP of a pool
   static constexpr int SLOT = X_BYTES + W_BYTES;
@@ -167,7 +173,7 @@ template <int RP> struct TcGeom {
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
   static constexpr int TM_COLS = 256;               // P: RP columns, output: 2 x 64
-  static constexpr int PER_THREAD = kTcOwn * RP / 4 / (32 * kTcWorkers);  // owned quads (at least 1)
+  static constexpr int PER_THREAD = OWN * RP / 4 / (32 * kTcWorkers);  // owned quads (at least 1)
 };
 
 struct TcBars {
@@ -191,11 +197,11 @@ struct TcBars {
 };
 
 // Worker warps (two per TMEM lane quadrant, thread = row of the tile).
-template <int XT, int UP, int RP>
+template <int XT, int UP, int RP, int CS>
 BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, int r16, int D, int U, bool patch, bool pad,
                             int o_begin, int o_end, int c_begin, int rank, uint32_t tmem, uint32_t sbase,
                             unsigned char *smem, const TcBars &B, volatile int *abort, cg::cluster_group &cluster) {
-  using G = TcGeom<RP>;
+  using G = TcGeom<RP, CS>;
   constexpr int NS = G::NS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = (int)threadIdx.x - 64;
   const int quad = warp & 3, half = (warp - 2) >> 2, m = quad * 32 + lane;
@@ -241,9 +247,10 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     ok = vote(mbar_wait(B.p_full, 0));
     tc_fence_after();
   }
+  cluster_wait();
   if (ok) {
-    const int rr = rank * kTcOwn + m % kTcOwn;
-    float *to = cluster.map_shared_rank(recv, m / kTcOwn) + rr * RP;
+    const int rr = rank * G::OWN + m % G::OWN;
+    float *to = cluster.map_shared_rank(recv, m / G::OWN) + rr * RP;
     for (int cgp = half; cgp < r16 / 16; cgp += 2) {
       float v[16];
       if (D > 0) {
@@ -258,7 +265,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
             make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
     }
     __syncwarp();
-    if (lane < kTcCS) mbar_arrive_cta(B.recv, lane);
+    if (lane < CS) mbar_arrive_cta(B.recv, lane);
     ok = vote(mbar_wait_cluster(B.recv, 0));
   }
   float own[G::PER_THREAD][4];
@@ -270,8 +277,8 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
       const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), chunk = i % (RP / 4), r = 4 * chunk;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (r < r_a)
-        for (int q = 0; q < kTcCS; ++q) {
-          const int rr = q * kTcOwn + ml;
+        for (int q = 0; q < CS; ++q) {
+          const int rr = q * G::OWN + ml;
           const float4 p = *reinterpret_cast<const float4 *>(recv + rr * RP + 4 * (chunk ^ (rr & 7)));
           v[0] += p.x;
           v[1] += p.y;
@@ -280,20 +287,20 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
         }
 #pragma unroll
       for (int j = 0; j < 4; ++j) own[k][j] = (r + j < r_a) ? v[j] * pre : 0.0f;
-      const int row = rank * kTcOwn + ml;
+      const int row = rank * G::OWN + ml;
       if (a.t && row < tile.rows && r < a.R)
         *reinterpret_cast<float4 *>(a.t + (int64_t)(tile.row0 + row) * a.R + r) =
             make_float4(own[k][0], own[k][1], own[k][2], own[k][3]);
     }
     __syncwarp();
-    if (lane < kTcCS) mbar_arrive_cta(B.taken, lane);  // this CTA's buffer may be overwritten by t
+    if (lane < CS) mbar_arrive_cta(B.taken, lane);  // this CTA's buffer may be overwritten by t
     ok = vote(mbar_wait_cluster(B.taken, 0));
   }
   if (ok) {
     const float post = (UP == 0) ? a.scales[tile.adapter] : 1.0f;  // to what the up step multiplies
 #pragma unroll
     for (int k = 0; k < G::PER_THREAD; ++k) {
-      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * kTcOwn + ml;
+      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * G::OWN + ml;
       float2 sc = make_float2(1.0f, 1.0f);
       if (XT == 0) {
         float mx = fmaxf(fmaxf(fabsf(own[k][0] * post), fabsf(own[k][1] * post)),
@@ -306,7 +313,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
       tc_split<XT>(own[k][0] * post * sc.y, own[k][1] * post * sc.y, hi.x, lo.x);
       tc_split<XT>(own[k][2] * post * sc.y, own[k][3] * post * sc.y, hi.y, lo.y);
       const int at = (r >> 6) * (kTcRows * 128) + row * 128 + ((((r & 63) >> 3) ^ (row & 7)) << 4) + (r & 7) * 2;
-      for (int q = 0; q < kTcCS; ++q) {
+      for (int q = 0; q < CS; ++q) {
         unsigned char *to = cluster.map_shared_rank(smem, q);
         if (r < r16) {
           *reinterpret_cast<uint2 *>(to + NS * G::SLOT + at) = hi;
@@ -317,83 +324,93 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     }
     fence_proxy_async_all();  // t is read by the tensor cores
     __syncwarp();
-    if (lane < kTcCS) mbar_arrive_cta(B.t_in, lane);
+    if (lane < CS) mbar_arrive_cta(B.t_in, lane);
     ok = vote(mbar_wait_cluster(B.t_in, 0));
     fence_proxy_async_all();
     __syncwarp();
     if (ok && lane == 0) mbar_arrive(B.t_ready);
   }
 
-  // ---- up: base + t W2, 64 columns a step, 32 per half ------------------------
+  // ---- up: base + t W2, 64 columns a step -------------------------------------
+  // The two warps of a quadrant take alternate steps (each its own buffer of
+  // tensor memory), so that one's waits hide behind the other's work: a step
+  // is a chain of waits, and with both warps on the same step it took 1.3 us.
   const float row_scale = (XT == 0 && ok) ? *reinterpret_cast<const float *>(smem + G::scale_off + 4 * m) : 1.0f;
-  for (int j = 0; j < U && ok; ++j) {
-    const int s = D + j, slot = s % NS, buf = j & 1;
+  uint16_t *out = a.y + (int64_t)(tile.row0 + quad * 32 + (lane >> 3)) * a.ldy + o_begin + 8 * (lane & 7);
+  for (int j = half; j < U && ok; j += 2) {
+    const int s = D + j, slot = s % NS;
     const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES;
     ok = vote(!*abort && mbar_wait(B.full + 8u * slot, (s / NS) & 1));
     if (!ok) break;
     if (patch) {
-      if (pad && UP == 0 && wt < 128) {  // W2 [64 rows][ranks]: zero ranks r_a .. r16 - 1
-        const int n = wt >> 1, r = r16 - 16 + 8 * (wt & 1), left = r_a - r;
-        if (left < 8) {
-          const uint32_t at = ws + (r >> 6) * 8192 + n * 128 + ((((r & 63) >> 3) ^ (n & 7)) << 4);
-          const uint4 v = lds_v4(at);
+      const int wg = quad * 32 + lane;
+      if (pad && UP == 0) {  // W2 [64 rows][ranks]: zero ranks r_a .. r16 - 1
+        const int n = wg >> 1, r = r16 - 16 + 8 * (wg & 1), live = r_a - r;
+        if (live < 8) {
+          const uint32_t wat = ws + (r >> 6) * 8192 + n * 128 + ((((r & 63) >> 3) ^ (n & 7)) << 4);
+          const uint4 v = lds_v4(wat);
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] &= (left > 2 * k + 1) ? 0xffffffffu : (left > 2 * k) ? 0x0000ffffu : 0u;
-          sts_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
+          for (int k = 0; k < 4; ++k) w[k] &= (live > 2 * k + 1) ? 0xffffffffu : (live > 2 * k) ? 0x0000ffffu : 0u;
+          sts_v4(wat, make_uint4(w[0], w[1], w[2], w[3]));
         }
       }
-      if (pad && UP == 1 && wt < 8 * (r16 - r_a)) sts_v4(ws + (r_a + (wt >> 3)) * 128 + (wt & 7) * 16, make_uint4(0, 0, 0, 0));
+      if (pad && UP == 1 && wg < 8 * (r16 - r_a)) sts_v4(ws + (r_a + (wg >> 3)) * 128 + (wg & 7) * 16, make_uint4(0, 0, 0, 0));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(B.masked + 8u * slot);
+      if (lane < 2) mbar_arrive(B.masked + 8u * slot);  // for the quadrant's other warp too
     }
-    ok = vote(mbar_wait(B.d_full + 8u * buf, (j >> 1) & 1));
+    ok = vote(mbar_wait(B.d_full + 8u * half, (j >> 1) & 1));
     if (!ok) break;
     tc_fence_after();
-    uint32_t d[32];
-    tmem_ld32(tmem + lane_addr + RP + 64 * buf + 32 * half, d);
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(B.d_empty + 8u * buf);
-    const int col0 = o_begin + 64 * j;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = 4 * half + q;
-      const uint32_t at = xs + m * 128 + ((c ^ (m & 7)) << 4);
-      uint4 b = make_uint4(0, 0, 0, 0);
-      if (a.base) b = lds_v4(at);
-      uint4 keep = make_uint4(0, 0, 0, 0);
-      if (UP == 1 && drop) keep = drop_block(dst, (uint32_t)(col0 >> 3) + c, (uint32_t)(tile.row0 + m));
-      const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-      uint32_t ow[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v0 = __uint_as_float(d[8 * q + 2 * i]), v1 = __uint_as_float(d[8 * q + 2 * i + 1]);
-        if (XT == 0) {
-          v0 *= row_scale;
-          v1 *= row_scale;
-        }
-        if (UP == 1 && drop) {
-          v0 = drop_keep(keep, 2 * i, dst.thr_hi) ? v0 * a.drop.inv_keep : 0.0f;
-          v1 = drop_keep(keep, 2 * i + 1, dst.thr_hi) ? v1 * a.drop.inv_keep : 0.0f;
-        }
-        const float2 bf = Elem<XT>::pair(bw[i]);
-        ow[i] = (uint32_t)Elem<XT>::from_float(bf.x + v0) | ((uint32_t)Elem<XT>::from_float(bf.y + v1) << 16);
+    for (int hc = 0; hc < 2; ++hc) {
+      uint32_t d[32];
+      tmem_ld32(tmem + lane_addr + RP + 64 * half + 32 * hc, d);
+      if (hc == 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.d_empty + 8u * half);
       }
-      sts_v4(at, make_uint4(ow[0], ow[1], ow[2], ow[3]));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t at = xs + m * 128 + (((4 * hc + q) ^ (m & 7)) << 4);
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (a.base) b = lds_v4(at);
+        if (UP == 1 && drop) {
+          const uint4 keep = drop_block(dst, (uint32_t)((o_begin >> 3) + 8 * j + 4 * hc + q), (uint32_t)(tile.row0 + m));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            d[8 * q + i] = drop_keep(keep, i, dst.thr_hi) ? __float_as_uint(__uint_as_float(d[8 * q + i]) * a.drop.inv_keep) : 0u;
+        }
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        uint32_t ow[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 v = make_float2(__uint_as_float(d[8 * q + 2 * i]), __uint_as_float(d[8 * q + 2 * i + 1]));
+          const float2 bf = Elem<XT>::pair(bw[i]);
+          v = XT == 0 ? __ffma2_rn(v, make_float2(row_scale, row_scale), bf) : __fadd2_rn(v, bf);
+          ow[i] = pack_pair<XT>(v);
+        }
+        sts_v4(at, make_uint4(ow[0], ow[1], ow[2], ow[3]));
+      }
     }
     __syncwarp();
-    // this warp's 32 rows x 64 bytes leave in whole sectors
+    // this warp's 32 rows x 128 bytes leave in whole lines; the slot is free
+    // (its next contents come by TMA) before the stores are under way
+    uint4 o[8];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int row = quad * 32 + it * 8 + (lane >> 2), c = 4 * half + (lane & 3), col = col0 + 8 * c;
-      if (row < tile.rows && col < o_end)
-        st_v4(a.y + (tile.row0 + row) * a.ldy + col, lds_v4(xs + row * 128 + ((c ^ (row & 7)) << 4)));
+    for (int q = 0; q < 8; ++q) {
+      const int row = quad * 32 + q * 4 + (lane >> 3);
+      o[q] = lds_v4(xs + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
     }
-    fence_proxy_async_smem();  // the slot's next contents come by TMA
+    fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(B.free_out + 8u * slot);
+    const bool in = o_begin + 64 * j + 8 * (lane & 7) < o_end;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (in && quad * 32 + q * 4 + (lane >> 3) < tile.rows) st_v4(out + (int64_t)(4 * q) * a.ldy + 64 * j, o[q]);
   }
   if (!ok && lane == 0) {
     if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
@@ -404,11 +421,11 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
 // grid = 8 x tiles, cluster = (8, 1, 1).  mx: x [M, Ci]; mA: A {K, R, L}, boxes
 // of 64 columns x 16 ranks; mB: B {R, N, L}, boxes of 64 ranks x 64 rows;
 // mbase: base [M, Co].
-template <int XT, int UP, int RP>
+template <int XT, int UP, int RP, int CS>
 __global__ void __launch_bounds__(kTcThreads, RP == 64 ? 2 : 1)
 lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mA,
                const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mbase, const LoraArgs a) {
-  using G = TcGeom<RP>;
+  using G = TcGeom<RP, CS>;
   constexpr int NS = G::NS;
   extern __shared__ __align__(1024) unsigned char tsm_raw[];
   const uint32_t raw = smem_u32(tsm_raw);
@@ -416,7 +433,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   unsigned char *smem = tsm_raw + (sbase - raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)blockIdx.x % kTcCS, tile_index = (int)blockIdx.x / kTcCS;
+  const int rank = (int)blockIdx.x % CS, tile_index = (int)blockIdx.x / CS;
   volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
   const TcBars B(sbase + G::bar_off, NS);
 
@@ -446,16 +463,16 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
       mbar_init(B.full + 8u * i, 1);
       mbar_init(B.masked + 8u * i, kTcWorkers);
       mbar_init(B.free_mma + 8u * i, 1);
-      mbar_init(B.free_out + 8u * i, kTcWorkers);
+      mbar_init(B.free_out + 8u * i, kTcWorkers / 2);
     }
     mbar_init(B.p_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(B.d_full + 8u * i, 1);
-      mbar_init(B.d_empty + 8u * i, kTcWorkers);
+      mbar_init(B.d_empty + 8u * i, kTcWorkers / 2);
     }
-    mbar_init(B.recv, kTcCS * kTcWorkers);
-    mbar_init(B.taken, kTcCS * kTcWorkers);
-    mbar_init(B.t_in, kTcCS * kTcWorkers);
+    mbar_init(B.recv, CS * kTcWorkers);
+    mbar_init(B.taken, CS * kTcWorkers);
+    mbar_init(B.t_in, CS * kTcWorkers);
     mbar_init(B.t_ready, kTcWorkers);
     mbar_init(B.done, 1);
     *abort = 0;
@@ -470,8 +487,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_arrive();  // barriers are initialised in every CTA before any remote arrival
-  cluster_wait();
+  cluster_arrive();  // barriers are initialised in every CTA before any remote arrival (the workers wait)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + G::tmem_off);
   const uint32_t t_smem = sbase + NS * G::SLOT;
 
@@ -510,6 +526,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
       for (int j = 1; j <= NS && j <= s; ++j) mbar_wait(B.full + 8u * ((s - j) % NS), ((s - j) / NS) & 1, 1u << 20);
     }
     __syncwarp();
+    cluster_wait();
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t ready = patch ? B.masked : B.full;
@@ -555,8 +572,9 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
       }
     }
     __syncwarp();
+    cluster_wait();
   } else {
-    lora_tc_workers<XT, UP, RP>(a, tile, r_a, r16, D, U, patch, pad, o_begin, o_end, c_begin, rank, tmem, sbase, smem, B,
+    lora_tc_workers<XT, UP, RP, CS>(a, tile, r_a, r16, D, U, patch, pad, o_begin, o_end, c_begin, rank, tmem, sbase, smem, B,
                                 abort, cluster);
   }
 
@@ -582,10 +600,10 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 //   dA[a] = sum_m dt[m]^T drop(x)[m]        [R, K]
 //   dB[a] = sum_m s_a dy[m]^T t[m]          [N, R]
 // Both are G[c, r] = sum_m X[m, c] P[m, r] over the rows of the adapter's
-// segments, X 16-bit and P fp32: tcgen05.mma with the column c as M = 128 and
+// segments, X 16-bit and P fp32: tcgen05.mma with the column c as M and
 // the rank as N, both operands MN-major (their rows run along the
 // contraction, as they lie in memory).  One launch does both gradients: a
-// cluster of 8 CTAs owns 128 columns of one adapter's dA or dB, its CTAs take
+// cluster owns CT columns (256 up to rank 64) of one adapter's dA or dB, its CTAs take
 // the adapter's 64-row tiles in turn, and their fp32 sums meet in distributed
 // shared memory in rank order: no atomics, no partial gradients in global
 // memory, and an adapter that occurs in several segments is summed by one
@@ -593,7 +611,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 // P enters as 16-bit parts side by side along N, so that one matrix
 // instruction multiplies all of them: bf16 three parts (24 bits); fp16 two,
 // P scaled by a power of two that brings the largest of the CTA's rows into
-// [2^14, 2^15).  X is read once; P once for each 128 columns (from L2).
+// [2^14, 2^15).  X is read once; P once for each CT columns (from L2).
 
 struct WgradSide {
   const float *P;     // [M, R]
@@ -608,20 +626,21 @@ struct WgradArgs {
   const float *scales;
   const int *seg_off, *seg_adapter;
   int64_t M;
-  int R, L, S;
+  int R, L, S, CS;  // CS: CTAs per cluster, 1, 2, 4 or 8
   DropArgs drop;  // on dA's X
 };
 
 constexpr int kWgRows = 64;   // rows per step
-constexpr int kWgCols = 128;  // columns per cluster (MMA M)
 
 template <int RP> struct WgradGeom {
-  static constexpr int X_BYTES = kWgRows * kWgCols * 2;
+  static constexpr int MB = (RP == 64) ? 2 : 1;          // MMAs of 128 columns (tensor memory holds the parts of both)
+  static constexpr int CT = 128 * MB;                    // columns per cluster
+  static constexpr int X_BYTES = kWgRows * CT * 2;
   static constexpr int PB = 3 * RP / 64;                 // 64-wide blocks of P's parts
   static constexpr int P_BYTES = PB * kWgRows * 128;
-  static constexpr int XS = (RP == 64) ? 3 : 4, PS = 2;  // stages
+  static constexpr int XS = 4, PS = 2;                   // stages
   static constexpr int RING = XS * X_BYTES + PS * P_BYTES;
-  static constexpr int RECV = kWgCols * RP * 4;
+  static constexpr int RECV = CT * RP * 4;
   static_assert(RECV <= RING, "the sums' buffer lies over the ring");
   static constexpr int bar_off = RING;
   static constexpr int nbar = 2 * XS + 2 * PS + 2;
@@ -629,12 +648,12 @@ template <int RP> struct WgradGeom {
   static constexpr int tmem_off = max_off + 4;
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
-  static constexpr int TM_COLS = (RP == 64) ? 256 : 512;
+  static constexpr int TM_COLS = 512;                    // MB x 3 RP columns in use
   static constexpr int PPT = kWgRows * RP / 4 / (32 * kTcWorkers);  // quads of P per worker
 };
 
 // The 64-row tiles of one adapter, in order: every warp walks all of them and
-// takes those whose number is its CTA's rank modulo 8.
+// takes those whose number is its CTA's rank modulo the cluster's size.
 struct WgradRows {
   int s0;            // first segment not looked at
   unsigned mask;     // segments of the last 32 that are left
@@ -666,7 +685,7 @@ BQ_DEV bool wgrad_next(WgradRows &w, const WgradArgs &a, int adapter, int rank) 
       w.cur_len = __shfl_sync(0xffffffffu, w.len, src);
     }
     // tiles count .. count + n - 1 are this segment's; skip to this CTA's
-    const int skip = (rank - w.count) & (kTcCS - 1);
+    const int skip = (rank - w.count) & (a.CS - 1);
     const int n = (w.cur_len + kWgRows - 1) / kWgRows;
     if (skip >= n) {
       w.count += n;
@@ -723,28 +742,28 @@ template <int XT> BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r1
   }
 }
 
-// grid = 8 x (L x (dA tiles + dB tiles)), cluster = (8, 1, 1); mx: x [M, K],
+// grid = CS x (L x (dA tiles + dB tiles)), cluster = (CS, 1, 1); mx: x [M, K],
 // mdy: dy [M, N], boxes of 64 columns x 16 rows.
 template <int XT, int RP>
-__global__ void __launch_bounds__(kTcThreads, RP == 64 ? 2 : 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
 lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mdy, const WgradArgs a) {
   using G = WgradGeom<RP>;
-  constexpr int XS = G::XS, PS = G::PS, PARTS = XT == 1 ? 3 : 2;
+  constexpr int XS = G::XS, PS = G::PS, PARTS = XT == 1 ? 3 : 2, CT = G::CT, MB = G::MB;
   extern __shared__ __align__(1024) unsigned char tsm_raw[];
   const uint32_t raw = smem_u32(tsm_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char *smem = tsm_raw + (sbase - raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)blockIdx.x % kTcCS, work = (int)blockIdx.x / kTcCS;
+  const int CS = a.CS, rank = (int)blockIdx.x % CS, work = (int)blockIdx.x / CS;
   const int per_adapter = a.dA.tiles + a.dB.tiles, adapter = work / per_adapter;
   const bool is_b = work % per_adapter >= a.dA.tiles;
   const WgradSide side = is_b ? a.dB : a.dA;
   const CUtensorMap *map = is_b ? &mdy : &mx;
-  const int c0 = (work % per_adapter - (is_b ? a.dA.tiles : 0)) * kWgCols;
+  const int c0 = (work % per_adapter - (is_b ? a.dA.tiles : 0)) * CT;
   const int r_a = lora_rank(a.ranks, adapter, a.L, a.R), r16 = (r_a + 15) & ~15;
   const int nfull = PARTS * r16, n0 = nfull < 192 ? nfull : 192, n1 = nfull - n0;  // columns of the two MMAs
-  const int cblocks = side.C - c0 > 64 ? 2 : 1;
+  const int cblocks = min(2 * MB, (side.C - c0 + 63) / 64);  // 64-column blocks in use
   const bool masked = !is_b && a.drop.thr != 0;
   volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
   const WgradBars B(sbase + G::bar_off, XS, PS);
@@ -819,10 +838,14 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + ps * G::P_BYTES;
         const int ks = (w.rows + 15) / 16;
         for (int k = 0; k < ks; ++k) {
-          const uint64_t xd = tc_desc(xb + 2048 * k, kWgRows * 128);
-          tc_mma(tmem, xd, tc_desc(pb + 2048 * k, kWgRows * 128), id0, steps > 0 || k > 0);
-          if (n1 > 0)
-            tc_mma(tmem + n0, xd, tc_desc(pb + 3 * (kWgRows * 128) + 2048 * k, kWgRows * 128), id1, steps > 0 || k > 0);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            if (2 * mb >= cblocks) break;
+            const uint64_t xd = tc_desc(xb + 2 * mb * (kWgRows * 128) + 2048 * k, kWgRows * 128);
+            tc_mma(tmem + mb * 192, xd, tc_desc(pb + 2048 * k, kWgRows * 128), id0, steps > 0 || k > 0);
+            if (MB == 1 && n1 > 0)
+              tc_mma(tmem + n0, xd, tc_desc(pb + 3 * (kWgRows * 128) + 2048 * k, kWgRows * 128), id1, steps > 0 || k > 0);
+          }
         }
         umma_commit(B.freed + 8u * slot);
         umma_commit(B.p_free + 8u * ps);
@@ -874,34 +897,41 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kTcWorkers) : "memory");
       pscale = tc_scale(__uint_as_float(*reinterpret_cast<volatile uint32_t *>(smem + G::max_off)));
     }
-    float4 pv[G::PPT];
-    bool more = wgrad_next(w, a, adapter, rank);
-    if (more) load_p(pv, w.row0, w.rows);
-    while (more) {
-      const int slot = steps % XS, ps = steps % PS, row0 = w.row0, rows = w.rows;
-      const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + ps * G::P_BYTES;
-      if (steps >= PS) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.p_free + 8u * ps, ((steps / PS) & 1) ^ 1)) != 0;
-      if (!ok) break;
+    // P is read two steps ahead (one step is shorter than the way to L2 and back)
+    float4 pv[2][G::PPT];
+    int row0[2], rows[2];
+    auto fetch = [&](int b) {
+      rows[b] = 0;
+      if (wgrad_next(w, a, adapter, rank)) {
+        row0[b] = w.row0;
+        rows[b] = w.rows;
+        load_p(pv[b], w.row0, w.rows);
+      }
+    };
+    auto step = [&](int b) {
+      const int slot = steps % XS, first = row0[b], n = rows[b];
+      const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + b * G::P_BYTES;
+      if (steps >= PS) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.p_free + 8u * b, ((steps / PS) & 1) ^ 1)) != 0;
+      if (!ok) return;
 #pragma unroll
       for (int k = 0; k < G::PPT; ++k) {
         const int i = wt + k * 32 * kTcWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
-        float4 v = pv[k];
+        float4 v = pv[b][k];
         if (XT == 0) v = make_float4(v.x * pscale.y, v.y * pscale.y, v.z * pscale.y, v.w * pscale.y);
         if (r < r16) wgrad_store_p<XT>(pb, m, r, r16, v);
       }
-      more = wgrad_next(w, a, adapter, rank);
-      if (more) load_p(pv, w.row0, w.rows);
-      const int rows16 = (rows + 15) & ~15;
-      if (masked || rows16 != rows) {
+      fetch(b);
+      const int rows16 = (n + 15) & ~15;
+      if (masked || rows16 != n) {
         ok = __all_sync(0xffffffffu, mbar_wait(B.full + 8u * slot, (steps / XS) & 1)) != 0;
-        if (!ok) break;
+        if (!ok) return;
         for (int i = wt; i < cblocks * rows16 * 8; i += 32 * kTcWorkers) {
-          const int c = i & 7, m = (i >> 3) % rows16, b = (i >> 3) / rows16;
-          const uint32_t at = xb + b * (kWgRows * 128) + m * 128 + ((c ^ (m & 7)) << 4);
-          if (m >= rows) {
+          const int c = i & 7, m = (i >> 3) % rows16, cb = (i >> 3) / rows16;
+          const uint32_t at = xb + cb * (kWgRows * 128) + m * 128 + ((c ^ (m & 7)) << 4);
+          if (m >= n) {
             sts_v4(at, make_uint4(0, 0, 0, 0));  // another segment's row
           } else if (masked) {
-            const uint4 g = drop_mask8(drop_block(dst, (uint32_t)(c0 >> 3) + 8 * b + c, (uint32_t)(row0 + m)), dst.thr_hi);
+            const uint4 g = drop_mask8(drop_block(dst, (uint32_t)(c0 >> 3) + 8 * cb + c, (uint32_t)(first + m)), dst.thr_hi);
             uint4 v = lds_v4(at);
             v.x &= g.x;
             v.y &= g.y;
@@ -913,8 +943,16 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(B.ready + 8u * ps);
+      if (lane == 0) mbar_arrive(B.ready + 8u * b);
       ++steps;
+    };
+    static_assert(PS == 2, "a register buffer for each stage of P");
+    fetch(0);
+    fetch(1);
+    while (ok && rows[0] > 0) {
+      step(0);
+      if (!ok || rows[1] <= 0) break;
+      step(1);
     }
     if (ok) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.d_full, 0)) != 0;
     if (!ok && lane == 0) {
@@ -937,11 +975,12 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
   cluster_arrive();
   cluster_wait();
   float *recv = reinterpret_cast<float *>(smem);
-  const int per_r = r16 / kTcCS;  // ranks of dA that one CTA owns (dB: 16 columns)
+  const int per_r = r16 / CS, own = CT / CS;  // ranks of dA / columns of dB that one CTA owns
   if (warp >= 2 && r_a > 0) {
-    const int quad = warp & 3, half = (warp - 2) >> 2, c = quad * 32 + lane;
-    const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
-    for (int cgp = half; cgp < r16 / 16; cgp += 2) {
+    // the two warps of a quadrant: one block of 128 columns each, or alternate ranks
+    const int quad = warp & 3, half = (warp - 2) >> 2, c = (MB == 2 ? half * 128 : 0) + quad * 32 + lane;
+    const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (MB == 2 ? half * 192 : 0);
+    for (int cgp = MB == 2 ? 0 : half; cgp < r16 / 16; cgp += 3 - MB) {
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0.0f;
@@ -962,10 +1001,10 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = cgp * 16 + i;
-          cluster.map_shared_rank(recv, r / per_r)[(rank * per_r + r % per_r) * kWgCols + c] = v[i];
+          cluster.map_shared_rank(recv, r / per_r)[(rank * per_r + r % per_r) * CT + c] = v[i];
         }
       } else {
-        float *to = cluster.map_shared_rank(recv, c / kTcOwn) + (rank * kTcOwn + c % kTcOwn) * RP;
+        float *to = cluster.map_shared_rank(recv, c / own) + (rank * own + c % own) * RP;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<float4 *>(to + 4 * ((cgp * 4 + q) ^ (c & 7))) =
@@ -986,16 +1025,16 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                        v.z != 0.0f ? v.z * scale : 0.0f, v.w != 0.0f ? v.w * scale : 0.0f);
   };
   if (!is_b) {
-    // this CTA's ranks (and, behind r16, every eighth zero row), 128 columns each
-    const int zero_rows = a.R > r16 ? (a.R - r16 - rank + kTcCS - 1) / kTcCS : 0;
-    for (int i = threadIdx.x; i < (per_r + zero_rows) * (kWgCols / 4); i += kTcThreads) {
-      const int rl = i / (kWgCols / 4), c = 4 * (i % (kWgCols / 4));
-      const int r = rl < per_r ? rank * per_r + rl : r16 + rank + (rl - per_r) * kTcCS;
+    // this CTA's ranks (and, behind r16, every CS-th zero row)
+    const int zero_rows = a.R > r16 ? (a.R - r16 - rank + CS - 1) / CS : 0;
+    for (int i = threadIdx.x; i < (per_r + zero_rows) * (CT / 4); i += kTcThreads) {
+      const int rl = i / (CT / 4), c = 4 * (i % (CT / 4));
+      const int r = rl < per_r ? rank * per_r + rl : r16 + rank + (rl - per_r) * CS;
       if (r >= a.R || c0 + c >= side.C) continue;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (r < r_a) {
-        for (int q = 0; q < kTcCS; ++q) {
-          const float4 p = *reinterpret_cast<const float4 *>(recv + (q * per_r + rl) * kWgCols + c);
+        for (int q = 0; q < CS; ++q) {
+          const float4 p = *reinterpret_cast<const float4 *>(recv + (q * per_r + rl) * CT + c);
           v.x += p.x;
           v.y += p.y;
           v.z += p.z;
@@ -1007,13 +1046,13 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     }
   } else {
     const int quads = a.R / 4;
-    for (int i = threadIdx.x; i < kTcOwn * quads; i += kTcThreads) {
-      const int cl = i / quads, chunk = i % quads, c = c0 + rank * kTcOwn + cl;
+    for (int i = threadIdx.x; i < own * quads; i += kTcThreads) {
+      const int cl = i / quads, chunk = i % quads, c = c0 + rank * own + cl;
       if (c >= side.C) continue;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (4 * chunk < r_a) {
-        for (int q = 0; q < kTcCS; ++q) {
-          const float4 p = *reinterpret_cast<const float4 *>(recv + (q * kTcOwn + cl) * RP + 4 * (chunk ^ (cl & 7)));
+        for (int q = 0; q < CS; ++q) {
+          const float4 p = *reinterpret_cast<const float4 *>(recv + (q * own + cl) * RP + 4 * (chunk ^ (cl & 7)));
           v.x += p.x;
           v.y += p.y;
           v.z += p.z;
