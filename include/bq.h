@@ -360,23 +360,52 @@ bq_status bq_dropout(const void *x, bq_dtype dtype, int64_t rows, int64_t cols, 
  * are multiples of 8 and rows 16-byte aligned, so a slice of a fused
  * projection can be x, base or y.  With BQ_OPT_LINEAR_OVERLAP >= 1 the kernel
  * takes part in the programmatic dependent launches of bq_linear.
- *
- * bq_lora: y[m] = base[m] + s_a (drop(x)[m] A_a^T) B_a^T.
- *   x        [M, K] of dtype (BQ_BF16 or BQ_F16), row stride ldx
- *   p, rng   dropout on x, as bq_dropout(x, p, rng) would give it before its
- *            rounding (p = 0: none, rng may be NULL)
- *   base     [M, N] of dtype, row stride ldbase; NULL: zeros.  May be y.
- *   y        [M, N] of dtype, row stride ldy; rows of segments are written in
- *            full (those without an adapter: base)
- *   t        NULL, or fp32 [M, R] (16-byte aligned) that receives
- *            t = drop(x) A_a^T, zero behind the rank, for bq_lora_grad
- * Products are exact and accumulated in fp32, t enters the second product
- * with a relative error below 2^-16, y is rounded once.  Deterministic.
+ * The arguments of one call, in host memory (read before the call returns):
  */
-bq_status bq_lora(const void *x, bq_dtype dtype, int64_t M, int64_t K, int64_t ldx, const void *A, const void *B,
-                  int64_t N, int R, int L, const int32_t *ranks, const float *scales, const int32_t *seg_off,
-                  const int32_t *seg_adapter, int S, double p, const uint64_t *rng, const void *base, int64_t ldbase,
-                  void *y, int64_t ldy, float *t, void *stream);
+typedef struct {
+    const void *x;               /* [M, K] of dtype, row stride ldx */
+    const void *A, *B;           /* pools */
+    const int32_t *ranks;
+    const float *scales;
+    const int32_t *seg_off, *seg_adapter;
+    const uint64_t *rng;         /* dropout on x, as in bq_dropout; NULL allowed when p rounds to 0 */
+    const void *base;            /* [M, N] of dtype, row stride ldbase; NULL: zeros.  May be y. */
+    void *y;                     /* [M, N] of dtype, row stride ldy */
+    float *t;                    /* NULL, or fp32 [M, R], 16-byte aligned: receives t for bq_lora_grad */
+    int64_t M, K, N, ldx, ldbase, ldy;
+    double p;                    /* dropout probability, as in bq_dropout */
+    int32_t R, L, S;
+    int32_t dtype;               /* BQ_BF16 or BQ_F16 */
+} bq_lora_args;
+
+typedef struct {
+    const void *dy;              /* [M, N] of dtype, row stride lddy */
+    const void *x;               /* the forward's x, row stride ldx; read for dA only */
+    const float *t;              /* fp32 [M, R] from the forward; read for dB only */
+    const void *A, *B;
+    const int32_t *ranks;
+    const float *scales;
+    const int32_t *seg_off, *seg_adapter;
+    const uint64_t *rng;         /* the forward's, unchanged */
+    const void *base;            /* [M, K] added to dx, row stride ldbase; NULL: zeros.  May be dx. */
+    void *dx;                    /* [M, K] of dtype, row stride lddx; NULL: not wanted */
+    float *dt;                   /* fp32 [M, R] scratch, needed for dx and dA; holds dt afterwards */
+    float *dA, *dB;              /* fp32 [L, R, K], [L, N, R]; NULL: not wanted */
+    int64_t M, K, N, lddy, ldx, ldbase, lddx;
+    double p;
+    int32_t R, L, S;
+    int32_t dtype;
+} bq_lora_grad_args;
+
+/*
+ * bq_lora: t[m] = drop(x)[m] A_a^T, y[m] = base[m] + s_a t[m] B_a^T.
+ * Dropout is what bq_dropout(x, p, rng) would give before its rounding.
+ * Rows of segments are written in full (those without an adapter: y = base,
+ * t = 0; t is 0 behind the rank).  Products are exact and accumulated in
+ * fp32, t enters the second product with a relative error below 2^-16, y is
+ * rounded once.  Deterministic.
+ */
+bq_status bq_lora(const bq_lora_args *args, void *stream);
 
 /*
  * bq_lora_grad: gradients of bq_lora with respect to x, A and B, from dy.
@@ -384,25 +413,13 @@ bq_status bq_lora(const void *x, bq_dtype dtype, int64_t M, int64_t K, int64_t l
  *     dx[m] = base[m] + mask / (1 - p) * (dt[m] A_a)
  *     dA_a  = sum over the adapter's rows of dt[m]^T drop(x)[m]     [L, R, K]
  *     dB_a  = sum over the adapter's rows of s_a dy[m]^T t[m]       [L, N, R]
- *   dy       [M, N] of dtype, row stride lddy
- *   x, t     the forward's input and the t that it stored (x is read for dA
- *            only, t for dB only); p, rng the forward's, unchanged
- *   base     [M, K] of dtype added to dx (bq_linear_grad_input's result), row
- *            stride ldbase; NULL: zeros.  May be dx.
- *   dx       [M, K] of dtype, row stride lddx, rows of segments written in
- *            full; NULL: not wanted
- *   dt       fp32 [M, R] scratch (16-byte aligned), needed for dx and dA; it
- *            holds dt afterwards.  Two calls in flight must not share it.
- *   dA, dB   fp32, written in full (zero behind the rank and for adapters
- *            without rows); NULL: not wanted
- * Segments, adapters, shapes and errors as above.  Sums over rows are fp32 in
- * a fixed order (deterministic, no atomics).
+ * base is bq_linear_grad_input's result, say.  Rows of segments of dx are
+ * written in full; dA and dB are written in full (zero behind the rank and
+ * for adapters without rows).  16-byte alignment for t, dt, dA and dB.  Two
+ * calls in flight must not share dt.  Sums over rows are fp32 in a fixed
+ * order (deterministic, no atomics).
  */
-bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int64_t lddy, const void *x, int64_t K,
-                       int64_t ldx, const float *t, const void *A, const void *B, int R, int L, const int32_t *ranks,
-                       const float *scales, const int32_t *seg_off, const int32_t *seg_adapter, int S, double p,
-                       const uint64_t *rng, const void *base, int64_t ldbase, void *dx, int64_t lddx, float *dt,
-                       float *dA, float *dB, void *stream);
+bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream);
 
 /*
  * Options.

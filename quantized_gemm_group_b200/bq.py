@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -89,14 +90,11 @@ def lib(path: str | None = None):
     L.bq_linear_ws.restype = i32
     L.bq_linear_grad_input.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, i32, i32, i64, i32, vp, vp]
     L.bq_linear_grad_input.restype = i32
-    f64 = ctypes.c_double
-    L.bq_dropout.argtypes = [vp, i32, i64, i64, i64, f64, vp, vp, i64, vp]
+    L.bq_dropout.argtypes = [vp, i32, i64, i64, i64, ctypes.c_double, vp, vp, i64, vp]
     L.bq_dropout.restype = i32
-    L.bq_lora.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, i32, vp, vp, vp, vp, i32, f64, vp, vp, i64, vp,
-                          i64, vp, vp]
+    L.bq_lora.argtypes = [ctypes.c_char_p, vp]
     L.bq_lora.restype = i32
-    L.bq_lora_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, f64,
-                               vp, vp, i64, vp, i64, vp, vp, vp, vp]
+    L.bq_lora_grad.argtypes = [ctypes.c_char_p, vp]
     L.bq_lora_grad.restype = i32
     L.bq_check_division.argtypes = [ctypes.c_uint32, ctypes.c_uint32, i32, vp, vp]
     L.bq_check_division.restype = i32
@@ -278,64 +276,64 @@ def bq_linear_grad_input(dy: torch.Tensor, packed, scales, zeros, K: int, bits: 
 # dropout and low-rank adapters
 # ---------------------------------------------------------------------------
 
-def _rows_ok(name, v, cols, dtype, device):
-    """v [M, cols] of dtype on device with unit column stride."""
-    if v.dim() != 2 or v.shape[1] != cols or v.dtype != dtype or v.device != device:
-        raise ValueError(f"{name}: [*, {cols}] {dtype} on {device} expected, got {tuple(v.shape)} {v.dtype} on {v.device}")
-    if cols > 1 and v.numel() and v.stride(1) != 1:
-        raise ValueError(f"{name}: columns must be contiguous")
+# bq_lora_args and bq_lora_grad_args of include/bq.h: pointers, then int64 sizes, then p and the int32 fields
+_LORA_ARGS = struct.Struct("=11Q6qd4i")
+_LORA_GRAD_ARGS = struct.Struct("=15Q7qd4i")
 
 
-def _dense(name, v, shape, dtype, device):
-    if tuple(v.shape) != shape or v.dtype != dtype or v.device != device or not v.is_contiguous():
-        raise ValueError(f"{name}: contiguous {shape} {dtype} on {device} expected, got {tuple(v.shape)} {v.dtype} "
-                         f"on {v.device}")
+def _bad(name: str, want: str, v):
+    return ValueError(f"{name}: {want} expected, got {tuple(v.shape)} {v.dtype} on {v.device} with strides {v.stride()}")
 
 
-def _rng_ptr(rng, device):
-    if rng is None:
-        return None
-    _dense("rng", rng, (2,), torch.int64, device)
-    return rng.data_ptr()
+def _matrix(name: str, v, rows: int, cols: int, dtype, dev: int) -> int:
+    """The row stride of v [rows, cols] of dtype on CUDA device dev, columns contiguous."""
+    if v.shape != (rows, cols) or v.dtype is not dtype or v.get_device() != dev:
+        raise _bad(name, f"[{rows}, {cols}] {dtype} on cuda:{dev}", v)
+    ld, unit = v.stride()
+    if unit != 1 and cols > 1 and rows:
+        raise _bad(name, "contiguous columns", v)
+    return ld
 
 
-def _launch(fn, name, device, stream, *args):
-    """Call `fn` on the tensors' device and its current stream (or `stream`)."""
-    if device.type != "cuda":
-        raise ValueError(f"{name}: CUDA tensors expected")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            st = fn(*args, s.cuda_stream)
-    else:
-        st = fn(*args, stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
-    _check(name, st)
+def _dense(name: str, v, shape, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this shape and dtype on CUDA device dev."""
+    if v.shape != shape or v.dtype is not dtype or v.get_device() != dev or not v.is_contiguous():
+        raise _bad(name, f"contiguous {shape} {dtype} on cuda:{dev}", v)
+    return v.data_ptr()
+
+
+def _rng_ptr(rng, dev: int) -> int:
+    return 0 if rng is None else _dense("rng", rng, (2,), torch.int64, dev)
+
+
+def _device(name: str, v) -> int:
+    dev = v.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor expected")
+    return dev
+
+
+def _launch(name: str, fn, dev: int, stream, *args):
+    """Call fn on the tensors' device, on its current stream or the one given."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _launch(name, fn, dev, stream, *args)
+    st = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    if st != BQ_OK:
+        raise BQError(name, st)
 
 
 def bq_dropout(x: torch.Tensor, p: float, rng=None, out=None, stream=None):
-    """mask * x / (1 - p) for x [rows, cols] (fp16 / bf16 / fp32, row stride free), the mask drawn
+    """mask * x / (1 - p) for x [rows, cols] (fp16 / bf16 / fp32, any row stride), the mask drawn
     from rng (int64 {seed, offset} on the device) and never stored.  The gradient is the same call on dy."""
     rows, cols = x.shape
-    _rows_ok("x", x, cols, x.dtype, x.device)
-    o = out if out is not None else torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    _rows_ok("out", o, cols, x.dtype, x.device)
-    if o.shape[0] != rows:
-        raise ValueError("out: as many rows as x expected")
-    _launch(lib().bq_dropout, "bq_dropout", x.device, stream, x.data_ptr(), DTYPE_CODE[x.dtype], rows, cols,
-            x.stride(0), p, _rng_ptr(rng, x.device), o.data_ptr(), o.stride(0))
-    return o
-
-
-def _adapters_ok(A, B, ranks, scales, seg_off, seg_adapter, K, N, dtype, device):
-    L, R = A.shape[0], A.shape[1]
-    S = seg_adapter.shape[0]
-    _dense("A", A, (L, R, K), dtype, device)
-    _dense("B", B, (L, N, R), dtype, device)
-    _dense("ranks", ranks, (L,), torch.int32, device)
-    _dense("scales", scales, (L,), torch.float32, device)
-    _dense("seg_off", seg_off, (S + 1,), torch.int32, device)
-    _dense("seg_adapter", seg_adapter, (S,), torch.int32, device)
-    return L, R, S
+    dev, dtype = _device("x", x), x.dtype
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=x.device)
+    _launch("bq_dropout", lib().bq_dropout, dev, stream, x.data_ptr(), DTYPE_CODE[dtype], rows, cols,
+            _matrix("x", x, rows, cols, dtype, dev), p, _rng_ptr(rng, dev), out.data_ptr(),
+            _matrix("out", out, rows, cols, dtype, dev))
+    return out
 
 
 def bq_lora(x: torch.Tensor, A, B, ranks, scales, seg_off, seg_adapter, base=None, out=None, p: float = 0.0, rng=None,
@@ -347,25 +345,22 @@ def bq_lora(x: torch.Tensor, A, B, ranks, scales, seg_off, seg_adapter, base=Non
     `out` holds.  base None: zeros; out may be base (in place) and is allocated when None.  t: fp32 [M, R] that
     receives drop(x) A[a]^T for bq_lora_grad."""
     M, K = x.shape
-    N, dtype, dev = B.shape[1], x.dtype, x.device
-    _rows_ok("x", x, K, dtype, dev)
-    L, R, S = _adapters_ok(A, B, ranks, scales, seg_off, seg_adapter, K, N, dtype, dev)
-    y = out
-    if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
-    for name, v in (("base", base), ("out", y)):
-        if v is not None:
-            _rows_ok(name, v, N, dtype, dev)
-            if v.shape[0] != M:
-                raise ValueError(f"{name}: {M} rows expected")
-    if t is not None:
-        _dense("t", t, (M, R), torch.float32, dev)
-    _launch(lib().bq_lora, "bq_lora", dev, stream, x.data_ptr(), DTYPE_CODE[dtype], M, K, x.stride(0), A.data_ptr(),
-            B.data_ptr(), N, R, L, ranks.data_ptr(), scales.data_ptr(), seg_off.data_ptr(), seg_adapter.data_ptr(), S, p,
-            _rng_ptr(rng, dev), base.data_ptr() if base is not None else None,
-            base.stride(0) if base is not None else 0, y.data_ptr(), y.stride(0),
-            t.data_ptr() if t is not None else None)
-    return y
+    L, N, R = B.shape
+    S, = seg_adapter.shape
+    dev, dtype = _device("x", x), x.dtype
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=x.device)
+    args = _LORA_ARGS.pack(
+        x.data_ptr(), _dense("A", A, (L, R, K), dtype, dev), _dense("B", B, (L, N, R), dtype, dev),
+        _dense("ranks", ranks, (L,), torch.int32, dev), _dense("scales", scales, (L,), torch.float32, dev),
+        _dense("seg_off", seg_off, (S + 1,), torch.int32, dev),
+        _dense("seg_adapter", seg_adapter, (S,), torch.int32, dev), _rng_ptr(rng, dev),
+        0 if base is None else base.data_ptr(), out.data_ptr(),
+        0 if t is None else _dense("t", t, (M, R), torch.float32, dev), M, K, N, _matrix("x", x, M, K, dtype, dev),
+        0 if base is None else _matrix("base", base, M, N, dtype, dev), _matrix("out", out, M, N, dtype, dev), p, R, L, S,
+        DTYPE_CODE[dtype])
+    _launch("bq_lora", lib().bq_lora, dev, stream, args)
+    return out
 
 
 def bq_lora_grad(dy: torch.Tensor, x, t, A, B, ranks, scales, seg_off, seg_adapter, base=None, out=None,
@@ -374,46 +369,47 @@ def bq_lora_grad(dy: torch.Tensor, x, t, A, B, ranks, scales, seg_off, seg_adapt
     """(dx, dA, dB) of bq_lora from dy [M, N], its input x, the t that it stored and the same p and rng.
 
     dx = base + mask / (1 - p) (scales[a] (dy B[a]) A[a]) in dy's dtype (base None: zeros; out may be base); dA [L, R, K]
-    and dB [L, N, R] in fp32, written in full.  need_dx / need_weights False skip them (None is returned).
-    workspace: fp32 [M, R] scratch, allocated when None."""
+    and dB [L, N, R] in fp32, written in full.  need_dx / need_weights False skip them (None is returned; x and t are
+    not looked at without the weights).  workspace: fp32 [M, R] scratch, allocated when None."""
     M, N = dy.shape
     L, R, K = A.shape
-    dtype, dev = dy.dtype, dy.device
-    _rows_ok("dy", dy, N, dtype, dev)
-    L, R, S = _adapters_ok(A, B, ranks, scales, seg_off, seg_adapter, K, N, dtype, dev)
+    S, = seg_adapter.shape
+    dev, dtype = _device("dy", dy), dy.dtype
+    if stream is not None and (workspace is None or (need_dx and out is None) or (need_weights and (dA is None or dB is None))):
+        # what is allocated here belongs to the stream that the kernels run on
+        with torch.cuda.stream(stream):
+            return bq_lora_grad(dy, x, t, A, B, ranks, scales, seg_off, seg_adapter, base, out, p, rng, dA, dB, workspace,
+                                need_dx, need_weights)
+    f32 = torch.float32
+    if workspace is None:
+        workspace = torch.empty((M, R), dtype=f32, device=dy.device)
+    xp = tp = bp = op = ap = wp = ldx = ldb = ldo = 0
+    if need_dx:
+        if out is None:
+            out = torch.empty((M, K), dtype=dtype, device=dy.device)
+        op, ldo = out.data_ptr(), _matrix("out", out, M, K, dtype, dev)
+        if base is not None:
+            bp, ldb = base.data_ptr(), _matrix("base", base, M, K, dtype, dev)
+    else:
+        out = None
     if need_weights:
-        _rows_ok("x", x, K, dtype, dev)
-        _dense("t", t, (M, R), torch.float32, dev)
-        if x.shape[0] != M:
-            raise ValueError(f"x: {M} rows expected")
-    # what is allocated here belongs to the stream that the kernels run on
-    with torch.cuda.stream(stream):
-        dx = None
-        if need_dx:
-            dx = out if out is not None else torch.empty((M, K), dtype=dtype, device=dev)
-            for name, v in (("base", base), ("out", dx)):
-                if v is not None:
-                    _rows_ok(name, v, K, dtype, dev)
-                    if v.shape[0] != M:
-                        raise ValueError(f"{name}: {M} rows expected")
-        if need_weights:
-            dA = dA if dA is not None else torch.empty((L, R, K), dtype=torch.float32, device=dev)
-            dB = dB if dB is not None else torch.empty((L, N, R), dtype=torch.float32, device=dev)
-            _dense("dA", dA, (L, R, K), torch.float32, dev)
-            _dense("dB", dB, (L, N, R), torch.float32, dev)
-        else:
-            dA = dB = None
-        ws = workspace if workspace is not None else torch.empty((M, R), dtype=torch.float32, device=dev)
-        _dense("workspace", ws, (M, R), torch.float32, dev)
-    ptr = lambda v: v.data_ptr() if v is not None else None  # noqa: E731
-    ld = lambda v: v.stride(0) if v is not None else 0  # noqa: E731
-    xx = x if need_weights else None
-    bb = base if need_dx else None
-    _launch(lib().bq_lora_grad, "bq_lora_grad", dev, stream, dy.data_ptr(), DTYPE_CODE[dtype], M, N, dy.stride(0),
-            ptr(xx), K, ld(xx), ptr(t if need_weights else None), A.data_ptr(), B.data_ptr(), R, L, ranks.data_ptr(),
-            scales.data_ptr(), seg_off.data_ptr(), seg_adapter.data_ptr(), S, p, _rng_ptr(rng, dev), ptr(bb), ld(bb),
-            ptr(dx), ld(dx), ws.data_ptr(), ptr(dA), ptr(dB))
-    return dx, dA, dB
+        if dA is None:
+            dA = torch.empty((L, R, K), dtype=f32, device=dy.device)
+        if dB is None:
+            dB = torch.empty((L, N, R), dtype=f32, device=dy.device)
+        ap, wp = _dense("dA", dA, (L, R, K), f32, dev), _dense("dB", dB, (L, N, R), f32, dev)
+        xp, ldx, tp = x.data_ptr(), _matrix("x", x, M, K, dtype, dev), _dense("t", t, (M, R), f32, dev)
+    else:
+        dA = dB = None
+    args = _LORA_GRAD_ARGS.pack(
+        dy.data_ptr(), xp, tp, _dense("A", A, (L, R, K), dtype, dev), _dense("B", B, (L, N, R), dtype, dev),
+        _dense("ranks", ranks, (L,), torch.int32, dev), _dense("scales", scales, (L,), f32, dev),
+        _dense("seg_off", seg_off, (S + 1,), torch.int32, dev),
+        _dense("seg_adapter", seg_adapter, (S,), torch.int32, dev), _rng_ptr(rng, dev), bp, op,
+        _dense("workspace", workspace, (M, R), f32, dev), ap, wp, M, K, N, _matrix("dy", dy, M, N, dtype, dev), ldx, ldb,
+        ldo, p, R, L, S, DTYPE_CODE[dtype])
+    _launch("bq_lora_grad", lib().bq_lora_grad, dev, stream, args)
+    return out, dA, dB
 
 
 def bq_check_division(s_bits_begin: int, s_bits_end: int, refinements: int = 2, stream=None):

@@ -1053,89 +1053,91 @@ bq_status bq_dropout(const void *x, bq_dtype dtype, int64_t rows, int64_t cols, 
   return launch_dropout<0>(x, rows, cols, ldx, out, ldo, d, st);
 }
 
-bq_status bq_lora(const void *x, bq_dtype dtype, int64_t M, int64_t K, int64_t ldx, const void *A, const void *B,
-                  int64_t N, int R, int L, const int32_t *ranks, const float *scales, const int32_t *seg_off,
-                  const int32_t *seg_adapter, int S, double p, const uint64_t *rng, const void *base, int64_t ldbase,
-                  void *y, int64_t ldy, float *t, void *stream) {
-  bq_status s = lora_check(dtype, M, K, N, R, L, S);
+bq_status bq_lora(const bq_lora_args *args, void *stream) {
+  if (!args) return BQ_ERR_NULL;
+  const bq_lora_args &q = *args;
+  const int64_t M = q.M, K = q.K, N = q.N;
+  const bq_dtype dtype = (bq_dtype)q.dtype;
+  bq_status s = lora_check(dtype, M, K, N, q.R, q.L, q.S);
   if (s != BQ_OK) return s;
   LoraArgs a = {};
-  if (!drop_args(p, rng, &a.drop)) return BQ_ERR_UNSUPPORTED;
-  if (M == 0 || S == 0) return BQ_OK;
-  if ((s = lora_matrix(x, M, K, ldx)) != BQ_OK) return s;
-  if ((s = lora_matrix(y, M, N, ldy)) != BQ_OK) return s;
-  if (base && (s = lora_matrix(base, M, N, ldbase)) != BQ_OK) return s;
-  if ((s = lora_matrix(A, L, K, K)) != BQ_OK || (s = lora_matrix(B, L, N, N)) != BQ_OK) return s;
-  if (!seg_off || !seg_adapter || (L && (!ranks || !scales)) || (a.drop.thr && !rng)) return BQ_ERR_NULL;
-  if (!aligned(seg_off, 4) || !aligned(seg_adapter, 4) || !aligned(ranks, 4) || !aligned(scales, 4) ||
-      !aligned(t, 16) || (a.drop.thr && !aligned(rng, 8)))
+  if (!drop_args(q.p, q.rng, &a.drop)) return BQ_ERR_UNSUPPORTED;
+  if (M == 0 || q.S == 0) return BQ_OK;
+  if ((s = lora_matrix(q.x, M, K, q.ldx)) != BQ_OK) return s;
+  if ((s = lora_matrix(q.y, M, N, q.ldy)) != BQ_OK) return s;
+  if (q.base && (s = lora_matrix(q.base, M, N, q.ldbase)) != BQ_OK) return s;
+  if ((s = lora_matrix(q.A, q.L, K, K)) != BQ_OK || (s = lora_matrix(q.B, q.L, N, N)) != BQ_OK) return s;
+  if (!q.seg_off || !q.seg_adapter || (q.L && (!q.ranks || !q.scales)) || (a.drop.thr && !q.rng)) return BQ_ERR_NULL;
+  if (!aligned(q.seg_off, 4) || !aligned(q.seg_adapter, 4) || !aligned(q.ranks, 4) || !aligned(q.scales, 4) ||
+      !aligned(q.t, 16) || (a.drop.thr && !aligned(q.rng, 8)))
     return BQ_ERR_ALIGN;
-  a.x = reinterpret_cast<const uint16_t *>(x);
-  a.A = reinterpret_cast<const uint16_t *>(A);
-  a.B = reinterpret_cast<const uint16_t *>(B);
-  a.base = reinterpret_cast<const uint16_t *>(base);
-  a.y = reinterpret_cast<uint16_t *>(y);
-  a.t = t;
-  a.ranks = ranks;
-  a.scales = scales;
-  a.seg_off = seg_off;
-  a.seg_adapter = seg_adapter;
+  a.x = reinterpret_cast<const uint16_t *>(q.x);
+  a.A = reinterpret_cast<const uint16_t *>(q.A);
+  a.B = reinterpret_cast<const uint16_t *>(q.B);
+  a.base = reinterpret_cast<const uint16_t *>(q.base);
+  a.y = reinterpret_cast<uint16_t *>(q.y);
+  a.t = q.t;
+  a.ranks = q.ranks;
+  a.scales = q.scales;
+  a.seg_off = q.seg_off;
+  a.seg_adapter = q.seg_adapter;
   a.M = M;
-  a.ldx = ldx;
-  a.ldbase = ldbase;
-  a.ldy = ldy;
+  a.ldx = q.ldx;
+  a.ldbase = q.ldbase;
+  a.ldy = q.ldy;
   a.Ci = (int)K;
   a.Co = (int)N;
-  a.R = R;
-  a.L = L;
-  a.S = S;
+  a.R = q.R;
+  a.L = q.L;
+  a.S = q.S;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == BQ_BF16 ? launch_lora<1, 0>(a, st) : launch_lora<0, 0>(a, st);
 }
 
-bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int64_t lddy, const void *x, int64_t K,
-                       int64_t ldx, const float *t, const void *A, const void *B, int R, int L, const int32_t *ranks,
-                       const float *scales, const int32_t *seg_off, const int32_t *seg_adapter, int S, double p,
-                       const uint64_t *rng, const void *base, int64_t ldbase, void *dx, int64_t lddx, float *dt,
-                       float *dA, float *dB, void *stream) {
+bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
+  if (!args) return BQ_ERR_NULL;
+  const bq_lora_grad_args &q = *args;
+  const int64_t M = q.M, K = q.K, N = q.N;
+  const bq_dtype dtype = (bq_dtype)q.dtype;
+  const int R = q.R, L = q.L, S = q.S;
   bq_status s = lora_check(dtype, M, K, N, R, L, S);
   if (s != BQ_OK) return s;
   LoraArgs a = {};
-  if (!drop_args(p, rng, &a.drop)) return BQ_ERR_UNSUPPORTED;
+  if (!drop_args(q.p, q.rng, &a.drop)) return BQ_ERR_UNSUPPORTED;
   const bool rows = M > 0 && S > 0;
-  const bool need_dt = dx || dA;
+  const bool need_dt = q.dx || q.dA;
   if (rows) {
-    if ((s = lora_matrix(dy, M, N, lddy)) != BQ_OK) return s;
-    if (dA && (s = lora_matrix(x, M, K, ldx)) != BQ_OK) return s;
-    if (dx && (s = lora_matrix(dx, M, K, lddx)) != BQ_OK) return s;
-    if (dx && base && (s = lora_matrix(base, M, K, ldbase)) != BQ_OK) return s;
-    if (dx && (s = lora_matrix(A, L, K, K)) != BQ_OK) return s;
-    if (need_dt && (s = lora_matrix(B, L, N, N)) != BQ_OK) return s;
-    if (!seg_off || !seg_adapter || (need_dt && !dt) || (dB && !t) || (a.drop.thr && !rng)) return BQ_ERR_NULL;
+    if ((s = lora_matrix(q.dy, M, N, q.lddy)) != BQ_OK) return s;
+    if (q.dA && (s = lora_matrix(q.x, M, K, q.ldx)) != BQ_OK) return s;
+    if (q.dx && (s = lora_matrix(q.dx, M, K, q.lddx)) != BQ_OK) return s;
+    if (q.dx && q.base && (s = lora_matrix(q.base, M, K, q.ldbase)) != BQ_OK) return s;
+    if (q.dx && (s = lora_matrix(q.A, L, K, K)) != BQ_OK) return s;
+    if (need_dt && (s = lora_matrix(q.B, L, N, N)) != BQ_OK) return s;
+    if (!q.seg_off || !q.seg_adapter || (need_dt && !q.dt) || (q.dB && !q.t) || (a.drop.thr && !q.rng)) return BQ_ERR_NULL;
   }
-  if (L && (!ranks || !scales)) return BQ_ERR_NULL;
-  if (!aligned(seg_off, 4) || !aligned(seg_adapter, 4) || !aligned(ranks, 4) || !aligned(scales, 4) ||
-      !aligned(t, 16) || !aligned(dt, 16) || !aligned(dA, 16) || !aligned(dB, 16) ||
-      (a.drop.thr && !aligned(rng, 8)))
+  if (L && (!q.ranks || !q.scales)) return BQ_ERR_NULL;
+  if (!aligned(q.seg_off, 4) || !aligned(q.seg_adapter, 4) || !aligned(q.ranks, 4) || !aligned(q.scales, 4) ||
+      !aligned(q.t, 16) || !aligned(q.dt, 16) || !aligned(q.dA, 16) || !aligned(q.dB, 16) ||
+      (a.drop.thr && !aligned(q.rng, 8)))
     return BQ_ERR_ALIGN;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (rows && need_dt) {
-    a.x = reinterpret_cast<const uint16_t *>(dy);
-    a.A = reinterpret_cast<const uint16_t *>(A);
-    a.B = reinterpret_cast<const uint16_t *>(B);
-    a.base = reinterpret_cast<const uint16_t *>(dx ? base : nullptr);
-    a.y = reinterpret_cast<uint16_t *>(dx);
-    a.t = dt;
-    a.ranks = ranks;
-    a.scales = scales;
-    a.seg_off = seg_off;
-    a.seg_adapter = seg_adapter;
+    a.x = reinterpret_cast<const uint16_t *>(q.dy);
+    a.A = reinterpret_cast<const uint16_t *>(q.A);
+    a.B = reinterpret_cast<const uint16_t *>(q.B);
+    a.base = reinterpret_cast<const uint16_t *>(q.dx ? q.base : nullptr);
+    a.y = reinterpret_cast<uint16_t *>(q.dx);
+    a.t = q.dt;
+    a.ranks = q.ranks;
+    a.scales = q.scales;
+    a.seg_off = q.seg_off;
+    a.seg_adapter = q.seg_adapter;
     a.M = M;
-    a.ldx = lddy;
-    a.ldbase = ldbase;
-    a.ldy = lddx;
+    a.ldx = q.lddy;
+    a.ldbase = q.ldbase;
+    a.ldy = q.lddx;
     a.Ci = (int)N;
-    a.Co = dx ? (int)K : 0;
+    a.Co = q.dx ? (int)K : 0;
     a.R = R;
     a.L = L;
     a.S = S;
@@ -1143,22 +1145,22 @@ bq_status bq_lora_grad(const void *dy, bq_dtype dtype, int64_t M, int64_t N, int
     if (s != BQ_OK) return s;
   }
   WgradArgs w = {};
-  w.dA.P = dt;
-  w.dA.out = dA;
+  w.dA.P = q.dt;
+  w.dA.out = q.dA;
   w.dA.C = (int)K;
-  w.dB.P = t;
-  w.dB.out = dB;
+  w.dB.P = q.t;
+  w.dB.out = q.dB;
   w.dB.C = (int)N;
-  w.ranks = ranks;
-  w.scales = scales;
-  w.seg_off = seg_off;
-  w.seg_adapter = seg_adapter;
+  w.ranks = q.ranks;
+  w.scales = q.scales;
+  w.seg_off = q.seg_off;
+  w.seg_adapter = q.seg_adapter;
   w.M = M;
   w.R = R;
   w.L = L;
   w.S = rows ? S : 0;
   w.drop = a.drop;
-  const WgradInputs in = {x, dy, M == 1 ? K : ldx, M == 1 ? N : lddy};
+  const WgradInputs in = {q.x, q.dy, M == 1 ? K : q.ldx, M == 1 ? N : q.lddy};
   if (dtype == BQ_BF16) return R <= 64 ? launch_wgrad<1, 64>(w, in, st) : launch_wgrad<1, 128>(w, in, st);
   return R <= 64 ? launch_wgrad<0, 64>(w, in, st) : launch_wgrad<0, 128>(w, in, st);
 }
