@@ -263,8 +263,6 @@ lora_kernel(LoraArgs a) {
     lora_copy_rows(a, tile, o_begin, o_end, rank == 0, kLoraThreads);
     return;
   }
-  // every CTA has started before any writes into its shared memory
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   const bool drop = a.drop.thr != 0;
   const DropState dst = drop_state(a.drop);
@@ -273,10 +271,12 @@ lora_kernel(LoraArgs a) {
   const uint16_t *poolB = a.B + (int64_t)tile.adapter * a.R * N;  // [N, R]
   const uint16_t *down = UP ? poolB : poolA;
   const int nt_used = (r_a + 7) / 8;
+  const int c_begin = rank * a.slice_c, c_end = min(a.Ci, c_begin + a.slice_c);
+  // every CTA has started before any writes into its shared memory
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // ---- down: partial sums of this warp's rows over its columns -------------
   const int rg = warp % RG, kq = warp / RG;
-  const int c_begin = rank * a.slice_c, c_end = min(a.Ci, c_begin + a.slice_c);
   const int steps = (c_end > c_begin) ? (c_end - c_begin + SC - 1) / SC : 0;
   const uint16_t *xrow[MT][2];
   bool xval[MT][2];
@@ -412,6 +412,55 @@ lora_kernel(LoraArgs a) {
       *reinterpret_cast<float2 *>(p) = make_float2(acc[mt][nt][0], acc[mt][nt][1]);
       *reinterpret_cast<float2 *>(p + 8 * RP) = make_float2(acc[mt][nt][2], acc[mt][nt][3]);
     }
+  // ---- up: this CTA's output columns, 32 per warp and turn -----------------
+  // A turn's pool elements are asked for a turn ahead (the first ones before the
+  // sums are exchanged): a turn is shorter than the way to L2 and back.
+  constexpr int MTU = BM / 16;             // 16-row tiles
+  constexpr int KC = (RP >= 32) ? RP / 32 : 1;  // runs of 32 ranks (one of 16 where RP = 16)
+  constexpr int KS = (RP >= 32) ? 2 : 1;   // k-steps in a run
+  constexpr int PER = 4 * KS;              // UP = 0: ranks that a lane holds of a run
+  constexpr int NV = (RP >= 32) ? RP / 8 : (UP == 0 ? 4 : 2);  // vectors per lane and turn
+  const int w_rows = (RP >= 32) ? (r_a + 31) & ~31 : 16;       // UP = 1: rows of A to stage
+  // UP = 1: the row of A in vector k of this lane; the eight rows of one store
+  // instruction lie in different banks
+  auto w_row = [&](int k) {
+    const int i8 = lane >> 2;
+    return (RP >= 32) ? 32 * (k >> 2) + 8 * (i8 >> 1) + 2 * (k & 3) + (i8 & 1) : 4 * (i8 >> 1) + 2 * k + (i8 & 1);
+  };
+  uint4 wv[NV];
+  auto load_w = [&](int cb) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) wv[k] = make_uint4(0, 0, 0, 0);
+    if (cb >= o_end) return;
+    if (UP == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = cb + 8 * (g >> 1) + 2 * j + (g & 1);
+        const uint16_t *p = poolB + (int64_t)n * a.R;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+          const int r = 32 * i + PER * t4;
+          if (n < o_end && r < r_a) {
+            if (KS == 2) {
+              wv[j * KC + i] = ld_nc_v4(p + r);
+            } else {
+              const uint2 q = *reinterpret_cast<const uint2 *>(p + r);
+              wv[j * KC + i].x = q.x;
+              wv[j * KC + i].y = q.y;
+            }
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int r = w_row(k), c = cb + 8 * (lane & 3);
+        if (r < r_a && c < o_end) wv[k] = ld_nc_v4(poolA + (int64_t)r * K + c);
+      }
+    }
+  };
+  load_w(o_begin + 32 * warp);
+
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   const int per = BM * RP / CS;  // elements that one CTA owns
@@ -463,71 +512,42 @@ lora_kernel(LoraArgs a) {
   }
   cluster.sync();
 
-  // ---- up: this CTA's output columns, 32 per warp and turn -----------------
-  constexpr int MTU = BM / 16;             // 16-row tiles
-  constexpr int KC = (RP >= 32) ? RP / 32 : 1;  // runs of 32 ranks (one of 16 where RP = 16)
-  constexpr int KS = (RP >= 32) ? 2 : 1;   // k-steps in a run
   const uint32_t tbase = sbase, wbase = sbase + G::T_BYTES + warp * G::WT_BYTES;
   const float out_scale = (UP == 1) ? a.drop.inv_keep : 1.0f;
   for (int cb = o_begin + 32 * warp; cb < o_end; cb += 32 * kLoraWarps) {
     uint32_t w[4][KC][KS][2];  // fragments of the up pool: n-tile, run, k-step
     if (UP == 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = cb + 8 * (g >> 1) + 2 * j + (g & 1);
-        const uint16_t *p = poolB + (int64_t)n * a.R;
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-          constexpr int PER = 4 * KS;  // ranks that a lane holds of a run
-          const int r = 32 * i + PER * t4, left = r_a - r;
-          uint32_t v[4] = {0, 0, 0, 0};
-          if (n < o_end && left > 0) {
-            if (KS == 2) {
-              const uint4 q = ld_nc_v4(p + r);
-              v[0] = q.x;
-              v[1] = q.y;
-              v[2] = q.z;
-              v[3] = q.w;
-            } else {
-              const uint2 q = *reinterpret_cast<const uint2 *>(p + r);
-              v[0] = q.x;
-              v[1] = q.y;
-            }
-            if (left < PER)  // what lies behind the rank may be anything
+          uint32_t v[4] = {wv[j * KC + i].x, wv[j * KC + i].y, wv[j * KC + i].z, wv[j * KC + i].w};
+          const int left = r_a - (32 * i + PER * t4);
+          if (left < PER)  // what lies behind the rank may be anything
 #pragma unroll
-              for (int k = 0; k < PER / 2; ++k)
-                v[k] &= (left > 2 * k + 1) ? 0xffffffffu : (left > 2 * k) ? 0x0000ffffu : 0u;
-          }
+            for (int k = 0; k < PER / 2; ++k)
+              v[k] &= (left > 2 * k + 1) ? 0xffffffffu : (left > 2 * k) ? 0x0000ffffu : 0u;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             w[j][i][ks][0] = v[2 * ks];
             w[j][i][ks][1] = v[2 * ks + 1];
           }
         }
-      }
     } else {
       // 32 columns of A [R, K], stored so that a transposed read gives the
       // column order above: pair p = 4 q + j of a row goes to tile j, place q
       __syncwarp();
-      const int rows = (RP >= 32) ? (r_a + 31) & ~31 : 16;
-      for (int i = lane; i < rows * 4; i += 32) {
-        const int q = i & 3;
-        // the eight rows of one store instruction lie in different banks
-        const int i8 = (i >> 2) & 7, blk = i >> 5;
-        int r;
-        if (RP >= 32) {
-          r = 32 * (blk >> 2) + 8 * (i8 >> 1) + 2 * (blk & 3) + (i8 & 1);
-        } else {
-          r = 4 * (i8 >> 1) + 2 * blk + (i8 & 1);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int r = w_row(k);
+        if (r < w_rows) {
+          const int f = (RP >= 32) ? (r >> 3) & 3 : (r >> 2) & 3;
+          const uint32_t at = wbase + r * 64 + (lane & 3) * 4;
+          sts_u32(at + ((0 ^ f) << 4), wv[k].x);
+          sts_u32(at + ((1 ^ f) << 4), wv[k].y);
+          sts_u32(at + ((2 ^ f) << 4), wv[k].z);
+          sts_u32(at + ((3 ^ f) << 4), wv[k].w);
         }
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < r_a && cb + 8 * q < o_end) v = ld_nc_v4(poolA + (int64_t)r * K + cb + 8 * q);
-        const int f = (RP >= 32) ? (r >> 3) & 3 : (r >> 2) & 3;
-        const uint32_t at = wbase + r * 64 + q * 4;
-        sts_u32(at + ((0 ^ f) << 4), v.x);
-        sts_u32(at + ((1 ^ f) << 4), v.y);
-        sts_u32(at + ((2 ^ f) << 4), v.z);
-        sts_u32(at + ((3 ^ f) << 4), v.w);
       }
       __syncwarp();
       const int l = lane & 7, hi = (lane >> 3) & 1, jx = lane >> 4;
@@ -548,6 +568,7 @@ lora_kernel(LoraArgs a) {
           }
         }
     }
+    load_w(cb + 32 * kLoraWarps);
     const int col = cb + 8 * t4;
 #pragma unroll
     for (int mt = 0; mt < MTU; ++mt) {
