@@ -957,37 +957,47 @@ bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
   return launch_cluster(kern, tiles * cs, cs, kLoraThreads, G::TOTAL, overlap_mode() >= 1, st, a);
 }
 
+// Clusters of cs CTAs that the GPU holds at once, two CTAs an SM, with what
+// clusters lose at the edges of the groups of SMs (148 SMs, asked of
+// cudaOccupancyMaxActiveClusters for a kernel of the same shared memory without
+// tensor memory: for kernels that use it the answer is one CTA an SM, but two
+// that share its 512 columns do run together).  per_sm = 1: one CTA an SM.
+int64_t cluster_places(int cs, int per_sm) {
+  static const int two[] = {0, 296, 148, 93, 71, 56, 45, 37, 33}, one[] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  return (int64_t)(per_sm == 2 ? two : one)[cs] * sm_count() / 148;
+}
+
 // Long segments: 128-row tiles on tcgen05.
-template <int XT, int UP, int RP, int CS>
+template <int XT, int UP, int RP>
 bq_status launch_lora_tc(LoraArgs a, cudaStream_t st) {
-  using G = TcGeom<RP, CS>;
+  using G = TcGeom<RP>;
   CUtensorMap mx = {}, mA = {}, mB = {}, mbase = {};
   const int64_t K = UP ? a.Co : a.Ci, N = UP ? a.Ci : a.Co;
   if (!make_map(&mx, a.x, XT == 1, a.Ci, a.M, 0, a.ldx, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
-  if (K && !make_map(&mA, a.A, XT == 1, K, a.R, a.L, K, (int64_t)a.R * K, 64, 16)) return BQ_ERR_CUDA;
+  if (K && !make_map(&mA, a.A, XT == 1, K, a.R, a.L, K, (int64_t)a.R * K, 64, (a.R + 15) & ~15)) return BQ_ERR_CUDA;
   if (N && !make_map(&mB, a.B, XT == 1, a.R, N, a.L, a.R, (int64_t)a.R * N, 64, 64)) return BQ_ERR_CUDA;
   if (a.base && a.Co && !make_map(&mbase, a.base, XT == 1, a.Co, a.M, 0, a.ldbase, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
-  a.CS = CS;
-  a.slice_c = (int)round_up((a.Ci + CS - 1) / CS, 64);
-  a.slice_o = (int)round_up((a.Co + CS - 1) / CS, 64);
-  constexpr auto kern = lora_tc_kernel<XT, UP, RP, CS>;
+  constexpr auto kern = lora_tc_kernel<XT, UP, RP>;
   if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
-  return launch_cluster(kern, lora_tiles(a, kTcRows) * CS, CS, kTcThreads, G::total, overlap_mode() >= 1, st, mx,
-                        mA, mB, mbase, a);
+  // The largest cluster with which all tiles are on the GPU at once: with one
+  // tile more than places the last one takes as long as all the others (72
+  // tiles in clusters of 4: 114 us, in clusters of 3: 88 us).
+  const int64_t tiles = lora_tiles(a, kTcRows);
+  int cs = kTcMaxCS;
+  while (cs > 1 && cluster_places(cs, RP == 64 ? 2 : 1) < tiles) --cs;
+  a.CS = cs;
+  return launch_cluster(kern, tiles * cs, cs, kTcThreads, G::total, overlap_mode() >= 1, st, mx, mA, mB, mbase, a);
 }
 
 template <int XT, int UP>
 bq_status launch_lora(const LoraArgs &a, cudaStream_t st) {
-  if (a.M == 0 || a.S == 0 || a.L == 0) return a.M && a.S ? launch_lora_t<XT, UP, 16>(a, st) : BQ_OK;
+  if (a.M == 0 || a.S == 0) return BQ_OK;
   // few rows a segment (or an empty contraction, which has no tensor map)
-  if (a.M <= 24 * (int64_t)a.S || a.Ci == 0) {
+  if (a.L == 0 || a.M <= 24 * (int64_t)a.S || a.Ci == 0) {
     if (a.R <= 16) return launch_lora_t<XT, UP, 16>(a, st);
     return a.R <= 64 ? launch_lora_t<XT, UP, 64>(a, st) : launch_lora_t<XT, UP, 128>(a, st);
   }
-  // clusters of 8 as long as they fit the GPU at once, else of 4
-  const bool wide = lora_tiles(a, kTcRows) * 8 <= (a.R <= 64 ? 2 : 1) * (int64_t)sm_count();
-  if (a.R <= 64) return wide ? launch_lora_tc<XT, UP, 64, 8>(a, st) : launch_lora_tc<XT, UP, 64, 4>(a, st);
-  return wide ? launch_lora_tc<XT, UP, 128, 8>(a, st) : launch_lora_tc<XT, UP, 128, 4>(a, st);
+  return a.R <= 64 ? launch_lora_tc<XT, UP, 64>(a, st) : launch_lora_tc<XT, UP, 128>(a, st);
 }
 
 struct WgradInputs {
@@ -1003,8 +1013,8 @@ bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, cudaStream_t st) {
   if (a.dB.out) a.dB.tiles = (a.dB.C + G::CT - 1) / G::CT;
   const int64_t clusters = (int64_t)a.L * (a.dA.tiles + a.dB.tiles);
   if (clusters == 0) return BQ_OK;
-  if (a.S && a.dA.tiles && !make_map(&mx, in.x, XT == 1, a.dA.C, a.M, 0, in.ldx, 0, 64, kTcWXBox)) return BQ_ERR_CUDA;
-  if (a.S && a.dB.tiles && !make_map(&mdy, in.dy, XT == 1, a.dB.C, a.M, 0, in.lddy, 0, 64, kTcWXBox)) return BQ_ERR_CUDA;
+  if (a.S && a.dA.tiles && !make_map(&mx, in.x, XT == 1, a.dA.C, a.M, 0, in.ldx, 0, 64, kWgRows)) return BQ_ERR_CUDA;
+  if (a.S && a.dB.tiles && !make_map(&mdy, in.dy, XT == 1, a.dB.C, a.M, 0, in.lddy, 0, 64, kWgRows)) return BQ_ERR_CUDA;
   constexpr auto kern = lora_wgrad_kernel<XT, RP>;
   if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
   // CTAs per cluster: enough to fill the GPU with the adapters that can be in

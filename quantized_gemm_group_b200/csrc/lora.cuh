@@ -125,26 +125,28 @@ BQ_DEV void lora_check_segments(const int *seg_off, const int *seg_adapter, cons
   if (bad) bq_flag(BQ_FLAG_BADMAP);
 }
 
-// Rows without a contribution: base's (nothing to do in place), t zero.  A
-// warp takes a row at a time, eight loads in flight a lane.
-BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int o_begin, int o_end, bool with_t, int threads) {
-  const int lane = threadIdx.x & 31;
-  if (a.base != a.y)
-    for (int m = threadIdx.x >> 5; m < tile.rows; m += threads >> 5) {
-      const uint16_t *from = a.base + (tile.row0 + m) * a.ldbase;
-      uint16_t *to = a.y + (tile.row0 + m) * a.ldy;
-      for (int c = o_begin + 8 * lane; c < o_end; c += 8 * 256) {
+// Rows without a contribution: base's (nothing to do in place), t zero.  The
+// cluster's warps take a row each in turn, eight loads in flight a lane.
+BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int rank, int CS, int threads) {
+  const int lane = threadIdx.x & 31, warps = threads >> 5;
+  for (int m = rank * warps + (threadIdx.x >> 5); m < tile.rows; m += CS * warps) {
+    const int64_t row = tile.row0 + m;
+    if (a.base != a.y) {
+      const uint16_t *from = a.base + row * a.ldbase;
+      uint16_t *to = a.y + row * a.ldy;
+      for (int c = 8 * lane; c < a.Co; c += 8 * 256) {
         uint4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          v[k] = (a.base && c + 256 * k < o_end) ? *reinterpret_cast<const uint4 *>(from + c + 256 * k) : make_uint4(0, 0, 0, 0);
+          v[k] = (a.base && c + 256 * k < a.Co) ? *reinterpret_cast<const uint4 *>(from + c + 256 * k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (c + 256 * k < o_end) st_v4(to + c + 256 * k, v[k]);
+          if (c + 256 * k < a.Co) st_v4(to + c + 256 * k, v[k]);
       }
     }
-  if (a.t && with_t)
-    for (int64_t i = threadIdx.x; i < (int64_t)tile.rows * a.R; i += threads) a.t[(int64_t)tile.row0 * a.R + i] = 0.0f;
+    if (a.t)
+      for (int i = lane; i < a.R; i += 32) a.t[row * a.R + i] = 0.0f;
+  }
 }
 
 // The rank to use: 0 (no contribution) without an adapter or with a bad one.
@@ -260,7 +262,7 @@ lora_kernel(LoraArgs a) {
   const int o_begin = rank * a.slice_o, o_end = min(a.Co, o_begin + a.slice_o);
 
   if (r_a == 0) {
-    lora_copy_rows(a, tile, o_begin, o_end, rank == 0, kLoraThreads);
+    lora_copy_rows(a, tile, rank, CS, kLoraThreads);
     return;
   }
 

@@ -42,8 +42,8 @@ namespace bq {
 constexpr int kTcRows = 128;                   // rows per tile (MMA M)
 constexpr int kTcWorkers = 8;                  // worker warps
 constexpr int kTcThreads = 32 * (2 + kTcWorkers);
-constexpr int kTcXBox = 32;                    // rows per TMA box of x and base
-constexpr int kTcWXBox = 16;                   // rows per TMA box of the weight gradients' X
+constexpr int kTcXBox = 64;                    // rows per TMA box of x and base
+constexpr int kTcMaxCS = 8;                    // CTAs per cluster at most
 
 // ---------------------------------------------------------------------------
 // primitives
@@ -109,7 +109,11 @@ BQ_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "mem
 BQ_DEV void sts_v4(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// 32 consecutive fp32 columns of this thread's TMEM lane, not yet waited for.
+BQ_DEV void tc_give_up(volatile int *abort) {  // a wait ran out: the other roles leave too
+  if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
+  *abort = 1;
+}
+// 32 consecutive fp32 columns of this thread's TMEM lane.
 BQ_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -157,15 +161,17 @@ BQ_DEV float2 tc_scale(float m) {
 // forward / input gradient
 // ---------------------------------------------------------------------------
 
-template <int RP, int CS> struct TcGeom {
-  static constexpr int OWN = kTcRows / CS;          // rows whose sums one CTA owns
+template <int RP> struct TcGeom {
   static constexpr int X_BYTES = kTcRows * 128;     // 128 rows x 64 columns
   static constexpr int W_BYTES = RP * 128;          // 64 x RP of a pool
   static constexpr int SLOT = X_BYTES + W_BYTES;
   static constexpr int NS = (RP == 64) ? 3 : 4;     // two CTAs per SM / one
   static constexpr int BLOCKS = RP / 64;            // 64-rank blocks
-  static constexpr int T_BYTES = 2 * BLOCKS * kTcRows * 128;  // hi and lo; the sums' buffer before
-  static constexpr int TOTAL0 = NS * SLOT + T_BYTES;
+  static constexpr int T_BYTES = 2 * BLOCKS * kTcRows * 128;  // hi and lo
+  // the sums' buffer lies there before: [CS][ceil(128 / CS) rows][RP] fp32, at most 133 rows
+  static constexpr int T_AREA = 136 * RP * 4;
+  static_assert(T_AREA >= T_BYTES, "t and the sums share their place");
+  static constexpr int TOTAL0 = NS * SLOT + T_AREA;
   static constexpr int bar_off = TOTAL0;
   static constexpr int nbar = 4 * NS + 10;
   static constexpr int scale_off = bar_off + 8 * nbar;  // fp32 per row
@@ -173,7 +179,7 @@ template <int RP, int CS> struct TcGeom {
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
   static constexpr int TM_COLS = 256;               // P: RP columns, output: 2 x 64
-  static constexpr int PER_THREAD = OWN * RP / 4 / (32 * kTcWorkers);  // owned quads (at least 1)
+  static constexpr int PER_THREAD = kTcRows * RP / 4 / (32 * kTcWorkers);  // quads of sums per worker, CS = 1
 };
 
 struct TcBars {
@@ -197,11 +203,11 @@ struct TcBars {
 };
 
 // Worker warps (two per TMEM lane quadrant, thread = row of the tile).
-template <int XT, int UP, int RP, int CS>
+template <int XT, int UP, int RP>
 BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, int r16, int D, int U, bool patch, bool pad,
-                            int o_begin, int o_end, int c_begin, int rank, uint32_t tmem, uint32_t sbase,
-                            unsigned char *smem, const TcBars &B, volatile int *abort, cg::cluster_group &cluster) {
-  using G = TcGeom<RP, CS>;
+                            int rank, uint32_t tmem, uint32_t sbase, unsigned char *smem, const TcBars &B, volatile int *abort, cg::cluster_group &cluster) {
+  const int CS = a.CS;
+  using G = TcGeom<RP>;
   constexpr int NS = G::NS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = (int)threadIdx.x - 64;
   const int quad = warp & 3, half = (warp - 2) >> 2, m = quad * 32 + lane;
@@ -223,7 +229,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
         for (int k = 0; k < kTcRows * 8 / (32 * kTcWorkers); ++k) {
           const int i = wt + k * 32 * kTcWorkers, row = i >> 3, c = i & 7;
           if (row >= tile.rows) continue;
-          const uint4 g = drop_mask8(drop_block(dst, (uint32_t)((c_begin >> 3) + 8 * s + c), (uint32_t)(tile.row0 + row)),
+          const uint4 g = drop_mask8(drop_block(dst, (uint32_t)(8 * (rank + CS * s) + c), (uint32_t)(tile.row0 + row)),
                                      dst.thr_hi);
           const uint32_t at = xs + row * 128 + ((c ^ (row & 7)) << 4);
           uint4 v = lds_v4(at);
@@ -240,8 +246,9 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     }
 
   // ---- the sums meet -------------------------------------------------------
-  // partial sums go to the owner of the row: [source CTA][16 rows][RP], 16-byte
+  // partial sums go to the owner of the row: [source CTA][own rows][RP], 16-byte
   // chunks XORed with the row so that a warp's rows lie in different banks
+  const int own = (kTcRows + CS - 1) / CS;
   float *recv = reinterpret_cast<float *>(smem + NS * G::SLOT);
   if (ok && D > 0) {
     ok = vote(mbar_wait(B.p_full, 0));
@@ -249,8 +256,8 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   }
   cluster_wait();
   if (ok) {
-    const int rr = rank * G::OWN + m % G::OWN;
-    float *to = cluster.map_shared_rank(recv, m / G::OWN) + rr * RP;
+    const int rr = rank * own + m % own;
+    float *to = cluster.map_shared_rank(recv, m / own) + rr * RP;
     for (int cgp = half; cgp < r16 / 16; cgp += 2) {
       float v[16];
       if (D > 0) {
@@ -268,17 +275,18 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     if (lane < CS) mbar_arrive_cta(B.recv, lane);
     ok = vote(mbar_wait_cluster(B.recv, 0));
   }
-  float own[G::PER_THREAD][4];
+  float sum[G::PER_THREAD][4];
   if (ok) {
     const float sc = a.scales[tile.adapter];
     const float pre = (UP == 0) ? a.drop.inv_keep : sc;  // to t (or dt) as stored
 #pragma unroll
     for (int k = 0; k < G::PER_THREAD; ++k) {
       const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), chunk = i % (RP / 4), r = 4 * chunk;
+      const int row = rank * own + ml;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (r < r_a)
+      if (ml < own && row < tile.rows && r < r_a)
         for (int q = 0; q < CS; ++q) {
-          const int rr = q * G::OWN + ml;
+          const int rr = q * own + ml;
           const float4 p = *reinterpret_cast<const float4 *>(recv + rr * RP + 4 * (chunk ^ (rr & 7)));
           v[0] += p.x;
           v[1] += p.y;
@@ -286,11 +294,10 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
           v[3] += p.w;
         }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) own[k][j] = (r + j < r_a) ? v[j] * pre : 0.0f;
-      const int row = rank * G::OWN + ml;
-      if (a.t && row < tile.rows && r < a.R)
+      for (int j = 0; j < 4; ++j) sum[k][j] = (r + j < r_a) ? v[j] * pre : 0.0f;
+      if (a.t && ml < own && row < tile.rows && r < a.R)
         *reinterpret_cast<float4 *>(a.t + (int64_t)(tile.row0 + row) * a.R + r) =
-            make_float4(own[k][0], own[k][1], own[k][2], own[k][3]);
+            make_float4(sum[k][0], sum[k][1], sum[k][2], sum[k][3]);
     }
     __syncwarp();
     if (lane < CS) mbar_arrive_cta(B.taken, lane);  // this CTA's buffer may be overwritten by t
@@ -300,27 +307,27 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     const float post = (UP == 0) ? a.scales[tile.adapter] : 1.0f;  // to what the up step multiplies
 #pragma unroll
     for (int k = 0; k < G::PER_THREAD; ++k) {
-      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * G::OWN + ml;
+      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * own + ml;
+      if (k * 32 * kTcWorkers >= own * (RP / 4)) break;
       float2 sc = make_float2(1.0f, 1.0f);
       if (XT == 0) {
-        float mx = fmaxf(fmaxf(fabsf(own[k][0] * post), fabsf(own[k][1] * post)),
-                         fmaxf(fabsf(own[k][2] * post), fabsf(own[k][3] * post)));
+        float mx = fmaxf(fmaxf(fabsf(sum[k][0] * post), fabsf(sum[k][1] * post)),
+                         fmaxf(fabsf(sum[k][2] * post), fabsf(sum[k][3] * post)));
 #pragma unroll
         for (int o = 1; o < RP / 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         sc = tc_scale(mx);
       }
       uint2 hi, lo;
-      tc_split<XT>(own[k][0] * post * sc.y, own[k][1] * post * sc.y, hi.x, lo.x);
-      tc_split<XT>(own[k][2] * post * sc.y, own[k][3] * post * sc.y, hi.y, lo.y);
+      tc_split<XT>(sum[k][0] * post * sc.y, sum[k][1] * post * sc.y, hi.x, lo.x);
+      tc_split<XT>(sum[k][2] * post * sc.y, sum[k][3] * post * sc.y, hi.y, lo.y);
       const int at = (r >> 6) * (kTcRows * 128) + row * 128 + ((((r & 63) >> 3) ^ (row & 7)) << 4) + (r & 7) * 2;
-      for (int q = 0; q < CS; ++q) {
-        unsigned char *to = cluster.map_shared_rank(smem, q);
-        if (r < r16) {
+      if (ml < own && row < kTcRows && r < r16)
+        for (int q = 0; q < CS; ++q) {
+          unsigned char *to = cluster.map_shared_rank(smem, q);
           *reinterpret_cast<uint2 *>(to + NS * G::SLOT + at) = hi;
           *reinterpret_cast<uint2 *>(to + NS * G::SLOT + G::BLOCKS * kTcRows * 128 + at) = lo;
+          if (XT == 0 && r == 0) *reinterpret_cast<float *>(to + G::scale_off + 4 * row) = sc.x;
         }
-        if (XT == 0 && r == 0) *reinterpret_cast<float *>(to + G::scale_off + 4 * row) = sc.x;
-      }
     }
     fence_proxy_async_all();  // t is read by the tensor cores
     __syncwarp();
@@ -336,10 +343,11 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   // tensor memory), so that one's waits hide behind the other's work: a step
   // is a chain of waits, and with both warps on the same step it took 1.3 us.
   const float row_scale = (XT == 0 && ok) ? *reinterpret_cast<const float *>(smem + G::scale_off + 4 * m) : 1.0f;
-  uint16_t *out = a.y + (int64_t)(tile.row0 + quad * 32 + (lane >> 3)) * a.ldy + o_begin + 8 * (lane & 7);
+  uint16_t *out = a.y + (int64_t)(tile.row0 + quad * 32 + (lane >> 3)) * a.ldy + 8 * (lane & 7);
   for (int j = half; j < U && ok; j += 2) {
     const int s = D + j, slot = s % NS;
     const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES;
+    const int col0 = 64 * (rank + CS * j);
     ok = vote(!*abort && mbar_wait(B.full + 8u * slot, (s / NS) & 1));
     if (!ok) break;
     if (patch) {
@@ -378,7 +386,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
         uint4 b = make_uint4(0, 0, 0, 0);
         if (a.base) b = lds_v4(at);
         if (UP == 1 && drop) {
-          const uint4 keep = drop_block(dst, (uint32_t)((o_begin >> 3) + 8 * j + 4 * hc + q), (uint32_t)(tile.row0 + m));
+          const uint4 keep = drop_block(dst, (uint32_t)((col0 >> 3) + 4 * hc + q), (uint32_t)(tile.row0 + m));
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             d[8 * q + i] = drop_keep(keep, i, dst.thr_hi) ? __float_as_uint(__uint_as_float(d[8 * q + i]) * a.drop.inv_keep) : 0u;
@@ -407,25 +415,24 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(B.free_out + 8u * slot);
-    const bool in = o_begin + 64 * j + 8 * (lane & 7) < o_end;
+    const bool in = col0 + 8 * (lane & 7) < a.Co;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (in && quad * 32 + q * 4 + (lane >> 3) < tile.rows) st_v4(out + (int64_t)(4 * q) * a.ldy + 64 * j, o[q]);
+      if (in && quad * 32 + q * 4 + (lane >> 3) < tile.rows) st_v4(out + (int64_t)(4 * q) * a.ldy + col0, o[q]);
   }
-  if (!ok && lane == 0) {
-    if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
-    *abort = 1;
-  }
+  if (!ok && lane == 0) tc_give_up(abort);
 }
 
-// grid = 8 x tiles, cluster = (8, 1, 1).  mx: x [M, Ci]; mA: A {K, R, L}, boxes
-// of 64 columns x 16 ranks; mB: B {R, N, L}, boxes of 64 ranks x 64 rows;
+// grid = CS x tiles, cluster = (CS, 1, 1).  mx: x [M, Ci]; mA: A {K, R, L}, boxes
+// of 64 columns x round_up(R, 16) ranks; mB: B {R, N, L}, boxes of 64 ranks x 64 rows;
 // mbase: base [M, Co].
-template <int XT, int UP, int RP, int CS>
-__global__ void __launch_bounds__(kTcThreads, RP == 64 ? 2 : 1)
+// Registers are handed out for whole groups of four warps, so two CTAs of 10
+// warps fit an SM as two of 12 do.
+template <int XT, int UP, int RP>
+__global__ void __launch_bounds__(RP == 64 ? 384 : kTcThreads, RP == 64 ? 2 : 1)
 lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mA,
                const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mbase, const LoraArgs a) {
-  using G = TcGeom<RP, CS>;
+  using G = TcGeom<RP>;
   constexpr int NS = G::NS;
   extern __shared__ __align__(1024) unsigned char tsm_raw[];
   const uint32_t raw = smem_u32(tsm_raw);
@@ -433,7 +440,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   unsigned char *smem = tsm_raw + (sbase - raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)blockIdx.x % CS, tile_index = (int)blockIdx.x / CS;
+  const int CS = a.CS, rank = (int)blockIdx.x % CS, tile_index = (int)blockIdx.x / CS;
   volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
   const TcBars B(sbase + G::bar_off, NS);
 
@@ -444,15 +451,14 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   const LoraTile tile = lora_find_tile<kTcRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
   if (!tile.found) return;  // the whole cluster
   const int r_a = lora_rank(a.ranks, tile.adapter, a.L, a.R);
-  const int o_begin = rank * a.slice_o, o_end = min(a.Co, o_begin + a.slice_o);
   if (r_a == 0) {
-    lora_copy_rows(a, tile, o_begin, o_end, rank == 0, kTcThreads);
+    lora_copy_rows(a, tile, rank, CS, kTcThreads);
     return;
   }
   const int r16 = (r_a + 15) & ~15;
-  const int c_begin = rank * a.slice_c, c_end = min(a.Ci, c_begin + a.slice_c);
-  const int D = c_end > c_begin ? (c_end - c_begin + 63) / 64 : 0;  // steps down
-  const int U = o_end > o_begin ? (o_end - o_begin + 63) / 64 : 0;  // steps up
+  // Steps down and up: the cluster's CTAs take the 64-column chunks of a row in
+  // turn, so that at any time they read and write neighbouring pieces of it.
+  const int D = ((a.Ci + 63) / 64 - rank + CS - 1) / CS, U = ((a.Co + 63) / 64 - rank + CS - 1) / CS;
   const bool drop = a.drop.thr != 0;
   const bool pad = (r_a & 15) != 0;                 // the last k-step of the up product needs zeros
   const bool patch = pad || (UP == 0 && drop);     // workers touch the slots before the MMA
@@ -493,34 +499,35 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 
   if (warp == 0) {
     if (lane == 0) {
-      const int boxes = (tile.rows + kTcXBox - 1) / kTcXBox;
-      int s = 0;
+      const int boxes = (tile.rows + kTcXBox - 1) / kTcXBox, ra16 = (a.R + 15) & ~15;
+      const uint32_t a_bytes = ra16 * 128, b_bytes = blocks * 8192, x_bytes = boxes * kTcXBox * 128;
+      int slot = 0, s = 0;
       for (; s < D + U; ++s) {
-        const int slot = s % NS, prev = s - NS;
-        if (prev >= 0) {
-          // the slot's last use: a step down is freed by its MMAs, a step up by the workers
-          const int first_up = D + (slot - D % NS + NS) % NS;  // first step up in this slot
-          const uint32_t bar = prev < D ? B.free_mma + 8u * slot : B.free_out + 8u * slot;
-          const int use = prev < D ? prev / NS : (prev - first_up) / NS;
-          if (*abort || !mbar_wait(bar, use & 1)) {
-            if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
-            *abort = 1;
-            break;
-          }
-        }
-        const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES, full = B.full + 8u * slot;
         const bool down = s < D;
-        const int c = down ? c_begin + 64 * s : o_begin + 64 * (s - D);
-        const bool from_a = down == (UP == 0);   // this step reads A (16-rank boxes), else B
+        const int prev = s - NS;
+        // the slot's last use: a step down is freed by its MMAs, a step up by the workers
+        if (prev >= 0 && !(prev < D ? mbar_wait(B.free_mma + 8u * slot, (prev / NS) & 1)
+                                    : mbar_wait(B.free_out + 8u * slot, ((prev - D) / NS) & 1))) {
+          tc_give_up(abort);
+          break;
+        }
+        const uint32_t xs = sbase + slot * G::SLOT, full = B.full + 8u * slot;
+        const int c = 64 * (rank + CS * (down ? s : s - D));
+        const bool from_a = down == (UP == 0);   // this step reads A, else B
         const bool rows_in = down || a.base;
-        mbar_arrive_expect_tx(full, (rows_in ? boxes * kTcXBox * 128 : 0) + (from_a ? r16 * 128 : blocks * 8192));
-        if (rows_in)
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(xs + i * kTcXBox * 128, down ? &mx : &mbase, c, tile.row0 + i * kTcXBox, full);
-        if (from_a)
-          for (int i = 0; i < r16 / 16; ++i) tma_load_3d(ws + i * 2048, &mA, c, i * 16, tile.adapter, full);
-        else
-          for (int i = 0; i < blocks; ++i) tma_load_3d(ws + i * 8192, &mB, i * 64, c, tile.adapter, full);
+        const CUtensorMap *map = down ? &mx : &mbase;
+        mbar_arrive_expect_tx(full, (rows_in ? x_bytes : 0) + (from_a ? a_bytes : b_bytes));
+        if (rows_in) {
+          tma_load_2d(xs, map, c, tile.row0, full);
+          if (boxes > 1) tma_load_2d(xs + kTcXBox * 128, map, c, tile.row0 + kTcXBox, full);
+        }
+        if (from_a) {
+          tma_load_3d(xs + G::X_BYTES, &mA, c, 0, tile.adapter, full);
+        } else {
+          tma_load_3d(xs + G::X_BYTES, &mB, 0, c, tile.adapter, full);
+          if (RP > 64 && blocks > 1) tma_load_3d(xs + G::X_BYTES + 8192, &mB, 64, c, tile.adapter, full);
+        }
+        if (++slot == NS) slot = 0;
       }
       // every copy has landed before the CTA may exit
       for (int j = 1; j <= NS && j <= s; ++j) mbar_wait(B.full + 8u * ((s - j) % NS), ((s - j) / NS) & 1, 1u << 20);
@@ -528,54 +535,71 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     __syncwarp();
     cluster_wait();
   } else if (warp == 1) {
+    // One thread issues everything, so a step is kept to its wait, its MMAs on
+    // running descriptors and a commit (built anew for each MMA they took 80
+    // cycles of this thread).
     if (lane == 0) {
       const uint32_t ready = patch ? B.masked : B.full;
       bool ok = true;
+      int slot = 0;
+      uint32_t use = 0;
+      const uint64_t xd0 = tc_desc(sbase, 16);
       // down: P [128 rows, r16] = x . W1, A operand x (K-major); W1 = A [r][64 c]
       // (K-major) forward, B [64 c][r] (MN-major) in the gradient
-      const uint32_t id_down = tc_idesc<XT>(r16, false, UP == 1);
-      for (int s = 0; s < D && ok; ++s) {
-        const int slot = s % NS;
-        ok = !*abort && mbar_wait(ready + 8u * slot, (s / NS) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES;
+      {
+        const uint32_t id = tc_idesc<XT>(r16, false, UP == 1);
+        const uint64_t wd0 = tc_desc(sbase + G::X_BYTES, UP == 0 ? 16 : 8192);
+        constexpr uint64_t KW = UP == 0 ? 2 : 128;  // a k-step of W1 in a descriptor's units of 16 bytes
+        bool more = false;
+        for (int s = 0; s < D; ++s) {
+          ok = mbar_wait(ready + 8u * slot, use);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t at = (uint64_t)(slot * (G::SLOT >> 4));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma(tmem, tc_desc(xs + 32 * k, 16), UP == 0 ? tc_desc(ws + 32 * k, 16) : tc_desc(ws + 2048 * k, 8192), id_down,
-                 s > 0 || k > 0);
-        umma_commit(B.free_mma + 8u * slot);
+          for (int k = 0; k < 4; ++k) {
+            tc_mma(tmem, xd0 + at + 2 * k, wd0 + at + KW * k, id, more);
+            more = true;
+          }
+          umma_commit(B.free_mma + 8u * slot);
+          if (++slot == NS) {
+            slot = 0;
+            use ^= 1;
+          }
+        }
+        if (ok && D > 0) umma_commit(B.p_full);
       }
-      if (ok && D > 0) umma_commit(B.p_full);
       // up: 64 output columns a step, A operand t (hi, then lo); W2 = B [64 c][r]
       // (K-major) forward, A [r][64 c] (MN-major) in the gradient
-      const uint32_t id_up = tc_idesc<XT>(64, false, UP == 1);
+      const uint32_t id = tc_idesc<XT>(64, false, UP == 1);
+      const uint64_t td = tc_desc(t_smem, 16), wd0 = tc_desc(sbase + G::X_BYTES, UP == 0 ? 16 : 8192);
+      const int ks = r16 / 16;
       if (ok && U > 0) ok = mbar_wait(B.t_ready, 0);
       for (int j = 0; j < U && ok; ++j) {
-        const int s = D + j, slot = s % NS, buf = j & 1;
-        ok = !*abort && mbar_wait(ready + 8u * slot, (s / NS) & 1) &&
-             (j < 2 || mbar_wait(B.d_empty + 8u * buf, ((j >> 1) & 1) ^ 1));
+        const int buf = j & 1;
+        ok = mbar_wait(ready + 8u * slot, use) && (j < 2 || mbar_wait(B.d_empty + 8u * buf, ((j >> 1) & 1) ^ 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ws = sbase + slot * G::SLOT + G::X_BYTES;
+        const uint64_t wd = wd0 + (uint64_t)(slot * (G::SLOT >> 4));
+#pragma unroll
         for (int part = 0; part < 2; ++part)
-          for (int k = 0; k < r16 / 16; ++k) {
-            const uint32_t ta = t_smem + (part * G::BLOCKS + k / 4) * (kTcRows * 128) + 32 * (k % 4);
-            const uint64_t wd = UP == 0 ? tc_desc(ws + (k / 4) * 8192 + 32 * (k % 4), 16) : tc_desc(ws + 2048 * k, 8192);
-            tc_mma(tmem + RP + 64 * buf, tc_desc(ta, 16), wd, id_up, part > 0 || k > 0);
-          }
+#pragma unroll
+          for (int k = 0; k < RP / 16; ++k)
+            if (k < ks)
+              tc_mma(tmem + RP + 64 * buf, td + (part * G::BLOCKS + k / 4) * (kTcRows * 128 >> 4) + 2 * (k % 4),
+                     UP == 0 ? wd + (k / 4) * 512 + 2 * (k % 4) : wd + 128 * k, id, part > 0 || k > 0);
         umma_commit(B.d_full + 8u * buf);
+        if (++slot == NS) {
+          slot = 0;
+          use ^= 1;
+        }
       }
-      if (!ok) {
-        if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
-        *abort = 1;
-      }
+      if (!ok) tc_give_up(abort);
     }
     __syncwarp();
     cluster_wait();
   } else {
-    lora_tc_workers<XT, UP, RP, CS>(a, tile, r_a, r16, D, U, patch, pad, o_begin, o_end, c_begin, rank, tmem, sbase, smem, B,
-                                abort, cluster);
+    lora_tc_workers<XT, UP, RP>(a, tile, r_a, r16, D, U, patch, pad, rank, tmem, sbase, smem, B, abort, cluster);
   }
 
   // everything issued by this CTA has finished before the tensor memory goes
@@ -743,7 +767,7 @@ template <int XT> BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r1
 }
 
 // grid = CS x (L x (dA tiles + dB tiles)), cluster = (CS, 1, 1); mx: x [M, K],
-// mdy: dy [M, N], boxes of 64 columns x 16 rows.
+// mdy: dy [M, N], boxes of 64 columns x 64 rows.
 template <int XT, int RP>
 __global__ void __launch_bounds__(kTcThreads, 1)
 lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mdy, const WgradArgs a) {
@@ -813,11 +837,10 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       }
       if (lane == 0) {
         const uint32_t xs = sbase + slot * G::X_BYTES, full = B.full + 8u * slot;
-        const int boxes = (w.rows + kTcWXBox - 1) / kTcWXBox;
-        mbar_arrive_expect_tx(full, cblocks * boxes * kTcWXBox * 128);
-        for (int b = 0; b < cblocks; ++b)
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(xs + b * (kWgRows * 128) + i * kTcWXBox * 128, map, c0 + 64 * b, w.row0 + i * kTcWXBox, full);
+        mbar_arrive_expect_tx(full, cblocks * (kWgRows * 128));
+#pragma unroll
+        for (int b = 0; b < 2 * MB; ++b)
+          if (b < cblocks) tma_load_2d(xs + b * (kWgRows * 128), map, c0 + 64 * b, w.row0, full);
       }
       __syncwarp();
       ++steps;
@@ -827,6 +850,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       mbar_wait(B.full + 8u * ((steps - j) % XS), ((steps - j) / XS) & 1, 1u << 20);
   } else if (warp == 1) {
     bool ok = true;
+    const uint64_t xd0 = tc_desc(sbase, kWgRows * 128), pd0 = tc_desc(sbase + XS * G::X_BYTES, kWgRows * 128);
     const uint32_t id0 = tc_idesc<XT>(n0, true, true), id1 = tc_idesc<XT>(n1 > 0 ? n1 : 16, true, true);
     while (wgrad_next(w, a, adapter, rank)) {
       const int slot = steps % XS, ps = steps % PS;
@@ -835,16 +859,17 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       if (!ok) break;
       if (lane == 0) {
         tc_fence_after();
-        const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + ps * G::P_BYTES;
+        const uint64_t xd = xd0 + (uint64_t)(slot * (G::X_BYTES >> 4)), pd = pd0 + (uint64_t)(ps * (G::P_BYTES >> 4));
         const int ks = (w.rows + 15) / 16;
-        for (int k = 0; k < ks; ++k) {
+#pragma unroll
+        for (int k = 0; k < kWgRows / 16; ++k) {
+          if (k >= ks) break;
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
             if (2 * mb >= cblocks) break;
-            const uint64_t xd = tc_desc(xb + 2 * mb * (kWgRows * 128) + 2048 * k, kWgRows * 128);
-            tc_mma(tmem + mb * 192, xd, tc_desc(pb + 2048 * k, kWgRows * 128), id0, steps > 0 || k > 0);
+            tc_mma(tmem + mb * 192, xd + 2 * mb * (kWgRows * 128 >> 4) + 128 * k, pd + 128 * k, id0, steps > 0 || k > 0);
             if (MB == 1 && n1 > 0)
-              tc_mma(tmem + n0, xd, tc_desc(pb + 3 * (kWgRows * 128) + 2048 * k, kWgRows * 128), id1, steps > 0 || k > 0);
+              tc_mma(tmem + n0, xd + 128 * k, pd + 3 * (kWgRows * 128 >> 4) + 128 * k, id1, steps > 0 || k > 0);
           }
         }
         umma_commit(B.freed + 8u * slot);
