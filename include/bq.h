@@ -318,8 +318,8 @@ bq_status bq_linear_grad_input(const void *dy, bq_dtype dtype, int64_t M, int64_
  * mask depends on (seed, offset, row, column) alone.
  *   x, out   [rows, cols] of dtype (BQ_F16, BQ_BF16 or BQ_F32), row strides
  *            ldx, ldo >= cols in elements; out may be x with ldo = ldx
- *            (no other overlap).  Any column count and alignment of whole
- *            elements; 16-byte aligned rows are the fast path.
+ *            (no other overlap).  Any column count (to 2^34, rows to 2^31) and
+ *            alignment of whole elements; 16-byte aligned rows are the fast path.
  *   p        probability of dropping an element, 0 <= p < 1, rounded to a
  *            multiple of 2^-16 (1 - 2^-17 and above: BQ_ERR_UNSUPPORTED)
  *   rng      DEVICE array {seed, offset}, read by the kernel, so that a captured

@@ -43,9 +43,9 @@ BQ_DEV DropState drop_state(const DropArgs &d) {
 BQ_DEV uint4 philox4x32_10(uint4 c, uint2 k) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint32_t h0 = __umulhi(0xD2511F53u, c.x), l0 = 0xD2511F53u * c.x;
-    const uint32_t h1 = __umulhi(0xCD9E8D57u, c.z), l1 = 0xCD9E8D57u * c.z;
-    c = make_uint4(h1 ^ c.y ^ k.x, l1, h0 ^ c.w ^ k.y, l0);
+    // one wide product each (the low and the high half apart are two)
+    const unsigned long long p0 = (unsigned long long)0xD2511F53u * c.x, p1 = (unsigned long long)0xCD9E8D57u * c.z;
+    c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ k.x, (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ k.y, (uint32_t)p0);
     k.x += 0x9E3779B9u;
     k.y += 0xBB67AE85u;
   }
@@ -74,37 +74,46 @@ BQ_DEV bool drop_keep(const uint4 &b, int i, uint32_t thr_hi) {
   return (i & 1) ? (w >= thr_hi) : ((w << 16) >= thr_hi);
 }
 
-template <int DT> struct DropElem {  // fp16, bf16
-  using T = uint16_t;
-  static BQ_DEV float load(T v) { return Elem<DT>::lo(v); }
-  static BQ_DEV T store(float v) { return Elem<DT>::from_float(v); }
-};
-template <> struct DropElem<2> {  // fp32
-  using T = float;
-  static BQ_DEV float load(T v) { return v; }
-  static BQ_DEV T store(float v) { return v; }
-};
+// Two floats rounded to a pair of fp16 (XT = 0) or bf16.
+template <int XT> BQ_DEV uint32_t pack_pair(float2 v) {
+  uint32_t r;
+  if (XT == 1) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+
+template <int DT> struct DropElem { using T = uint16_t; };  // fp16, bf16
+template <> struct DropElem<2> { using T = float; };
 
 // One thread takes blocks of 8 columns, grid-stride over rows x blocks, kUnroll
 // loads in flight.  VEC: both matrices have 16-byte aligned rows, whole blocks
 // move as 16-byte vectors (the last block of a ragged row element by element).
+// fp32 runs at the rate of a copy; 16-bit types are bound by the generator's
+// instructions, so places advance by additions and pairs are scaled, rounded
+// and masked together (8192 x 14336 bf16, p = 0.05: 110 -> 89 us; p = 0 73 us).
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(256)
-dropout_kernel(const typename DropElem<DT>::T *x, int64_t rows, int64_t cols, int64_t ldx,
+__global__ void __launch_bounds__(256, 5)
+dropout_kernel(const typename DropElem<DT>::T *x, uint32_t rows, int64_t cols, int64_t ldx,
                typename DropElem<DT>::T *out, int64_t ldo, DropArgs d) {
-  using E = DropElem<DT>;
-  using T = typename E::T;
+  using T = typename DropElem<DT>::T;
   constexpr int kVecs = (int)(8 * sizeof(T) / 16);
   constexpr int kUnroll = 2;
   const DropState st = drop_state(d);
-  const int64_t blocks = (cols + 7) / 8, total = rows * blocks;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  int64_t idx = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  // (row, blk) advance with the index without a division a step
-  const int64_t drow = step / blocks, dblk = step - drow * blocks;
-  int64_t row = idx / blocks, blk = idx - row * blocks;
-  while (idx < total) {
-    int64_t r[kUnroll], b[kUnroll];
+  const uint32_t blocks = (uint32_t)((cols + 7) / 8);
+  const bool ragged = (cols & 7) != 0;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x, first = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  // row, block and both places advance with the index
+  const uint32_t drow = (uint32_t)(step / blocks), dblk = (uint32_t)(step - (int64_t)drow * blocks);
+  const int64_t dx = drow * ldx + 8 * (int64_t)dblk, dout = drow * ldo + 8 * (int64_t)dblk;
+  const int64_t wrap_x = ldx - 8 * (int64_t)blocks, wrap_o = ldo - 8 * (int64_t)blocks;
+  int64_t row64 = first / blocks;
+  if (row64 >= rows) return;
+  uint32_t row = (uint32_t)row64, blk = (uint32_t)(first - row64 * blocks);
+  const T *src = x + row * ldx + 8 * (int64_t)blk;
+  T *dst = out + row * ldo + 8 * (int64_t)blk;
+  while (row < rows) {
+    uint32_t r[kUnroll], b[kUnroll];
+    T *to[kUnroll];
     bool act[kUnroll], full[kUnroll];
     union {
       T e[8];
@@ -112,46 +121,58 @@ dropout_kernel(const typename DropElem<DT>::T *x, int64_t rows, int64_t cols, in
     } buf[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      act[u] = idx < total;
       r[u] = row;
       b[u] = blk;
-      full[u] = VEC && (8 * blk + 8 <= cols);
+      to[u] = dst;
+      act[u] = row < rows;
+      full[u] = VEC && !(ragged && blk == blocks - 1);
       if (act[u]) {
-        const T *src = x + row * ldx + 8 * blk;
         if (full[u]) {
 #pragma unroll
           for (int k = 0; k < kVecs; ++k) buf[u].v[k] = reinterpret_cast<const uint4 *>(src)[k];
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (8 * blk + i < cols) buf[u].e[i] = src[i];
+            if (8 * (int64_t)blk + i < cols) buf[u].e[i] = src[i];
         }
       }
-      idx += step;
       row += drow;
       blk += dblk;
+      src += dx;
+      dst += dout;
       if (blk >= blocks) {
         blk -= blocks;
         ++row;
+        src += wrap_x;
+        dst += wrap_o;
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (!act[u]) continue;
       if (d.thr) {
-        const uint4 g = drop_block(st, (uint32_t)b[u], (uint32_t)r[u]);
+        const uint4 g = drop_block(st, b[u], r[u]);
+        if constexpr (sizeof(T) == 2) {  // pairs: scaled and rounded together, then masked
+          const uint4 k = drop_mask8(g, st.thr_hi);
+          const float2 f = make_float2(d.inv_keep, d.inv_keep);
+          uint4 v = buf[u].v[0];
+          v.x = pack_pair<DT>(__fmul2_rn(Elem<DT>::pair(v.x), f)) & k.x;
+          v.y = pack_pair<DT>(__fmul2_rn(Elem<DT>::pair(v.y), f)) & k.y;
+          v.z = pack_pair<DT>(__fmul2_rn(Elem<DT>::pair(v.z), f)) & k.z;
+          v.w = pack_pair<DT>(__fmul2_rn(Elem<DT>::pair(v.w), f)) & k.w;
+          buf[u].v[0] = v;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          buf[u].e[i] = drop_keep(g, i, st.thr_hi) ? E::store(E::load(buf[u].e[i]) * d.inv_keep) : T(0);
+          for (int i = 0; i < 8; ++i) buf[u].e[i] = drop_keep(g, i, st.thr_hi) ? buf[u].e[i] * d.inv_keep : T(0);
+        }
       }
-      T *dst = out + r[u] * ldo + 8 * b[u];
       if (full[u]) {
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) reinterpret_cast<uint4 *>(dst)[k] = buf[u].v[k];
+        for (int k = 0; k < kVecs; ++k) reinterpret_cast<uint4 *>(to[u])[k] = buf[u].v[k];
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (8 * b[u] + i < cols) dst[i] = buf[u].e[i];
+          if (8 * (int64_t)b[u] + i < cols) to[u][i] = buf[u].e[i];
       }
     }
   }

@@ -126,13 +126,6 @@ BQ_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Two floats rounded to a pair of type XT.
-template <int XT> BQ_DEV uint32_t pack_pair(float2 v) {
-  if (XT == 1) return pack_bf16(v.x, v.y);
-  const __half2 h = __floats2half2_rn(v.x, v.y);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // Two floats as the hi and lo parts of type XT (fp16: scaled by the caller).
 template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t &lo) {
   if (XT == 1) {
