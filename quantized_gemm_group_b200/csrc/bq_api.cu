@@ -1022,7 +1022,7 @@ bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, cudaStream_t st) {
   const int64_t busy = (int64_t)(a.S < a.L ? a.S : a.L) * (a.dA.tiles + a.dB.tiles);
   a.CS = 1;
   while (a.CS < 8 && 2 * busy * a.CS <= (int64_t)sm_count()) a.CS *= 2;
-  return launch_cluster(kern, clusters * a.CS, a.CS, kTcThreads, G::total, false, st, mx, mdy, a);
+  return launch_cluster(kern, clusters * a.CS, a.CS, kWgThreads, G::total, false, st, mx, mdy, a);
 }
 
 // What bq_lora and bq_lora_grad have in common.

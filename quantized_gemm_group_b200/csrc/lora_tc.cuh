@@ -106,6 +106,7 @@ BQ_DEV bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
 BQ_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 BQ_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 BQ_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+BQ_DEV uint4 and4(uint4 a, uint4 b) { return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w); }
 BQ_DEV void sts_v4(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -210,27 +211,29 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   bool ok = true;
   auto vote = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
 
-  // ---- down: masks on x ----------------------------------------------------
+  // ---- down: masks on x (drawn while x is on its way) -----------------------
   if (patch)
     for (int s = 0; s < D && ok; ++s) {
       const int slot = s % NS;
+      constexpr int PT = kTcRows * 8 / (32 * kTcWorkers);  // 16-byte chunks per worker
+      uint4 mask[PT];
+      if (UP == 0 && drop) {
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+          const int i = wt + k * 32 * kTcWorkers;
+          mask[k] = drop_mask8(drop_block(dst, (uint32_t)(8 * (rank + CS * s) + (i & 7)), (uint32_t)(tile.row0 + (i >> 3))),
+                               dst.thr_hi);
+        }
+      }
       ok = vote(!*abort && mbar_wait(B.full + 8u * slot, (s / NS) & 1));
       if (!ok) break;
       if (UP == 0 && drop) {
         const uint32_t xs = sbase + slot * G::SLOT;
 #pragma unroll
-        for (int k = 0; k < kTcRows * 8 / (32 * kTcWorkers); ++k) {
-          const int i = wt + k * 32 * kTcWorkers, row = i >> 3, c = i & 7;
-          if (row >= tile.rows) continue;
-          const uint4 g = drop_mask8(drop_block(dst, (uint32_t)(8 * (rank + CS * s) + c), (uint32_t)(tile.row0 + row)),
-                                     dst.thr_hi);
-          const uint32_t at = xs + row * 128 + ((c ^ (row & 7)) << 4);
-          uint4 v = lds_v4(at);
-          v.x &= g.x;
-          v.y &= g.y;
-          v.z &= g.z;
-          v.w &= g.w;
-          sts_v4(at, v);
+        for (int k = 0; k < PT; ++k) {
+          const int i = wt + k * 32 * kTcWorkers, row = i >> 3;
+          const uint32_t at = xs + row * 128 + (((i & 7) ^ (row & 7)) << 4);
+          sts_v4(at, and4(lds_v4(at), mask[k]));
         }
         fence_proxy_async_smem();
       }
@@ -647,7 +650,10 @@ struct WgradArgs {
   DropArgs drop;  // on dA's X
 };
 
-constexpr int kWgRows = 64;   // rows per step
+constexpr int kWgRows = 64;      // rows per step
+constexpr int kWgGroups = 4;     // worker warps per TMEM lane quadrant
+constexpr int kWgWorkers = 4 * kWgGroups;
+constexpr int kWgThreads = 32 * (2 + kWgWorkers);
 
 template <int RP> struct WgradGeom {
   static constexpr int MB = (RP == 64) ? 2 : 1;          // MMAs of 128 columns (tensor memory holds the parts of both)
@@ -666,7 +672,7 @@ template <int RP> struct WgradGeom {
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
   static constexpr int TM_COLS = 512;                    // MB x 3 RP columns in use
-  static constexpr int PPT = kWgRows * RP / 4 / (32 * kTcWorkers);  // quads of P per worker
+  static constexpr int PPT = kWgRows * RP / 4 / (32 * kWgWorkers);  // quads of P per worker
 };
 
 // The 64-row tiles of one adapter, in order: every warp walks all of them and
@@ -762,7 +768,7 @@ template <int XT> BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r1
 // grid = CS x (L x (dA tiles + dB tiles)), cluster = (CS, 1, 1); mx: x [M, K],
 // mdy: dy [M, N], boxes of 64 columns x 64 rows.
 template <int XT, int RP>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kWgThreads, 1)
 lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mdy, const WgradArgs a) {
   using G = WgradGeom<RP>;
   constexpr int XS = G::XS, PS = G::PS, PARTS = XT == 1 ? 3 : 2, CT = G::CT, MB = G::MB;
@@ -791,7 +797,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       mbar_init(B.freed + 8u * i, 1);
     }
     for (int i = 0; i < PS; ++i) {
-      mbar_init(B.ready + 8u * i, kTcWorkers);
+      mbar_init(B.ready + 8u * i, kWgWorkers);
       mbar_init(B.p_free + 8u * i, 1);
     }
     mbar_init(B.d_full, 1);
@@ -886,7 +892,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     auto load_p = [&](float4 (&pv)[G::PPT], int row0, int rows) {
 #pragma unroll
       for (int k = 0; k < G::PPT; ++k) {
-        const int i = wt + k * 32 * kTcWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
+        const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
         pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (m < rows && r < r_a) {
           pv[k] = *reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r);
@@ -912,7 +918,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       }
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
       if (lane == 0) atomicMax(reinterpret_cast<unsigned *>(smem + G::max_off), __float_as_uint(mx));
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kTcWorkers) : "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWgWorkers) : "memory");
       pscale = tc_scale(__uint_as_float(*reinterpret_cast<volatile uint32_t *>(smem + G::max_off)));
     }
     // P is read two steps ahead (one step is shorter than the way to L2 and back)
@@ -933,29 +939,26 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       if (!ok) return;
 #pragma unroll
       for (int k = 0; k < G::PPT; ++k) {
-        const int i = wt + k * 32 * kTcWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
+        const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
         float4 v = pv[b][k];
         if (XT == 0) v = make_float4(v.x * pscale.y, v.y * pscale.y, v.z * pscale.y, v.w * pscale.y);
         if (r < r16) wgrad_store_p<XT>(pb, m, r, r16, v);
       }
       fetch(b);
-      const int rows16 = (n + 15) & ~15;
-      if (masked || rows16 != n) {
+      if (masked || (n & 15)) {
+        constexpr int PT = 2 * MB * kWgRows * 8 / (32 * kWgWorkers);  // 16-byte chunks per worker
         ok = __all_sync(0xffffffffu, mbar_wait(B.full + 8u * slot, (steps / XS) & 1)) != 0;
         if (!ok) return;
-        for (int i = wt; i < cblocks * rows16 * 8; i += 32 * kTcWorkers) {
-          const int c = i & 7, m = (i >> 3) % rows16, cb = (i >> 3) / rows16;
-          const uint32_t at = xb + cb * (kWgRows * 128) + m * 128 + ((c ^ (m & 7)) << 4);
+#pragma unroll 2
+        for (int k = 0; k < PT; ++k) {
+          const int i = wt + k * 32 * kWgWorkers, m = (i >> 3) % kWgRows, cb = i / (8 * kWgRows);
+          const uint32_t at = xb + cb * (kWgRows * 128) + m * 128 + (((i & 7) ^ (m & 7)) << 4);
+          if (cb >= cblocks) continue;
           if (m >= n) {
             sts_v4(at, make_uint4(0, 0, 0, 0));  // another segment's row
           } else if (masked) {
-            const uint4 g = drop_mask8(drop_block(dst, (uint32_t)(c0 >> 3) + 8 * cb + c, (uint32_t)(first + m)), dst.thr_hi);
-            uint4 v = lds_v4(at);
-            v.x &= g.x;
-            v.y &= g.y;
-            v.z &= g.z;
-            v.w &= g.w;
-            sts_v4(at, v);
+            const uint4 q = drop_block(dst, (uint32_t)(c0 >> 3) + 8 * cb + (i & 7), (uint32_t)(first + m));
+            sts_v4(at, and4(lds_v4(at), drop_mask8(q, dst.thr_hi)));
           }
         }
       }
@@ -995,10 +998,10 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
   float *recv = reinterpret_cast<float *>(smem);
   const int per_r = r16 / CS, own = CT / CS;  // ranks of dA / columns of dB that one CTA owns
   if (warp >= 2 && r_a > 0) {
-    // the two warps of a quadrant: one block of 128 columns each, or alternate ranks
-    const int quad = warp & 3, half = (warp - 2) >> 2, c = (MB == 2 ? half * 128 : 0) + quad * 32 + lane;
-    const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (MB == 2 ? half * 192 : 0);
-    for (int cgp = MB == 2 ? 0 : half; cgp < r16 / 16; cgp += 3 - MB) {
+    // the warps of a quadrant share its blocks of 128 columns and the ranks
+    const int quad = warp & 3, grp = (warp - 2) >> 2, mb = MB == 2 ? grp & 1 : 0, c = mb * 128 + quad * 32 + lane;
+    const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + mb * 192;
+    for (int cgp = grp / MB; cgp < r16 / 16; cgp += kWgGroups / MB) {
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0.0f;
@@ -1045,7 +1048,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
   if (!is_b) {
     // this CTA's ranks (and, behind r16, every CS-th zero row)
     const int zero_rows = a.R > r16 ? (a.R - r16 - rank + CS - 1) / CS : 0;
-    for (int i = threadIdx.x; i < (per_r + zero_rows) * (CT / 4); i += kTcThreads) {
+    for (int i = threadIdx.x; i < (per_r + zero_rows) * (CT / 4); i += kWgThreads) {
       const int rl = i / (CT / 4), c = 4 * (i % (CT / 4));
       const int r = rl < per_r ? rank * per_r + rl : r16 + rank + (rl - per_r) * CS;
       if (r >= a.R || c0 + c >= side.C) continue;
@@ -1064,7 +1067,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     }
   } else {
     const int quads = a.R / 4;
-    for (int i = threadIdx.x; i < own * quads; i += kTcThreads) {
+    for (int i = threadIdx.x; i < own * quads; i += kWgThreads) {
       const int cl = i / quads, chunk = i % quads, c = c0 + rank * own + cl;
       if (c >= side.C) continue;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
