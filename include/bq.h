@@ -403,7 +403,7 @@ typedef struct {
  * Rows of segments are written in full (those without an adapter: y = base,
  * t = 0; t is 0 behind the rank).  Products are exact and accumulated in
  * fp32, t enters the second product with a relative error below 2^-16, y is
- * rounded once.  Deterministic.
+ * rounded once.  y and t do not overlap x.  Deterministic.
  */
 bq_status bq_lora(const bq_lora_args *args, void *stream);
 
@@ -416,8 +416,8 @@ bq_status bq_lora(const bq_lora_args *args, void *stream);
  * base is bq_linear_grad_input's result, say.  Rows of segments of dx are
  * written in full; dA and dB are written in full (zero behind the rank and
  * for adapters without rows).  16-byte alignment for t, dt, dA and dB.  Two
- * calls in flight must not share dt.  Sums over rows are fp32 in a fixed
- * order (deterministic, no atomics).
+ * calls in flight must not share dt.  No output overlaps dy, x or t.  Sums
+ * over rows are fp32 in a fixed order (deterministic, no atomics).
  */
 bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream);
 

@@ -1006,7 +1006,7 @@ struct WgradInputs {
 };
 
 template <int XT, int RP>
-bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, cudaStream_t st) {
+bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, bool after_dt, cudaStream_t st) {
   using G = WgradGeom<RP>;
   CUtensorMap mx = {}, mdy = {};
   if (a.dA.out) a.dA.tiles = (a.dA.C + G::CT - 1) / G::CT;
@@ -1022,7 +1022,7 @@ bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, cudaStream_t st) {
   const int64_t busy = (int64_t)(a.S < a.L ? a.S : a.L) * (a.dA.tiles + a.dB.tiles);
   a.CS = 1;
   while (a.CS < 8 && 2 * busy * a.CS <= (int64_t)sm_count()) a.CS *= 2;
-  return launch_cluster(kern, clusters * a.CS, a.CS, kWgThreads, G::total, false, st, mx, mdy, a);
+  return launch_cluster(kern, clusters * a.CS, a.CS, kWgThreads, G::total, after_dt, st, mx, mdy, a);
 }
 
 // What bq_lora and bq_lora_grad have in common.
@@ -1171,8 +1171,10 @@ bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
   w.S = rows ? S : 0;
   w.drop = a.drop;
   const WgradInputs in = {q.x, q.dy, M == 1 ? K : q.ldx, M == 1 ? N : q.lddy};
-  if (dtype == BQ_BF16) return R <= 64 ? launch_wgrad<1, 64>(w, in, st) : launch_wgrad<1, 128>(w, in, st);
-  return R <= 64 ? launch_wgrad<0, 64>(w, in, st) : launch_wgrad<0, 128>(w, in, st);
+  // launched over the kernel that makes dt (dB's part does not wait for it)
+  const bool after_dt = rows && need_dt;
+  if (dtype == BQ_BF16) return R <= 64 ? launch_wgrad<1, 64>(w, in, after_dt, st) : launch_wgrad<1, 128>(w, in, after_dt, st);
+  return R <= 64 ? launch_wgrad<0, 64>(w, in, after_dt, st) : launch_wgrad<0, 128>(w, in, after_dt, st);
 }
 
 }  // extern "C"

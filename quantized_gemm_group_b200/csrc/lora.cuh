@@ -70,7 +70,7 @@ struct LoraTile {
 
 // A segment as the kernels use it: its length, 0 where the offsets are unusable.
 BQ_DEV int lora_segment(const int *seg_off, int s, int64_t M, int *start) {
-  const int a = seg_off[s], b = seg_off[s + 1];
+  const int a = __ldcg(seg_off + s), b = __ldcg(seg_off + s + 1);
   *start = a;
   return (a >= 0 && b >= a && b <= M) ? b - a : 0;
 }
@@ -86,7 +86,7 @@ BQ_DEV LoraTile lora_find_tile(const int *seg_off, const int *seg_adapter, int S
     const int s = s0 + lane;
     int start = 0, len = 0, ad = -1;
     if (s < S) {
-      ad = seg_adapter[s];
+      ad = __ldcg(seg_adapter + s);
       len = lora_segment(seg_off, s, M, &start);
     }
     const int n = (len + BM - 1) / BM;
@@ -152,7 +152,7 @@ BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int rank, in
 // The rank to use: 0 (no contribution) without an adapter or with a bad one.
 BQ_DEV int lora_rank(const int *ranks, int adapter, int L, int R) {
   if (adapter < 0 || adapter >= L) return 0;
-  const int r = ranks[adapter];
+  const int r = __ldcg(ranks + adapter);
   return (r < 0 || r > R) ? 0 : r;
 }
 
@@ -252,8 +252,8 @@ lora_kernel(LoraArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const uint32_t sbase = smem_u32(smem);
 
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // everything before this kernel is complete
   if (blockIdx.x == 0 && warp == kLoraWarps - 1)
     lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
   const LoraTile tile = lora_find_tile<BM>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);

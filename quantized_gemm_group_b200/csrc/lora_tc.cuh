@@ -103,6 +103,9 @@ BQ_DEV bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
+BQ_DEV void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 BQ_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 BQ_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 BQ_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -440,26 +443,6 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
   const TcBars B(sbase + G::bar_off, NS);
 
-  pdl_launch_dependents();
-  pdl_wait();
-  if (blockIdx.x == 0 && warp == kTcWorkers + 1)
-    lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
-  const LoraTile tile = lora_find_tile<kTcRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
-  if (!tile.found) return;  // the whole cluster
-  const int r_a = lora_rank(a.ranks, tile.adapter, a.L, a.R);
-  if (r_a == 0) {
-    lora_copy_rows(a, tile, rank, CS, kTcThreads);
-    return;
-  }
-  const int r16 = (r_a + 15) & ~15;
-  // Steps down and up: the cluster's CTAs take the 64-column chunks of a row in
-  // turn, so that at any time they read and write neighbouring pieces of it.
-  const int D = ((a.Ci + 63) / 64 - rank + CS - 1) / CS, U = ((a.Co + 63) / 64 - rank + CS - 1) / CS;
-  const bool drop = a.drop.thr != 0;
-  const bool pad = (r_a & 15) != 0;                 // the last k-step of the up product needs zeros
-  const bool patch = pad || (UP == 0 && drop);     // workers touch the slots before the MMA
-  const int blocks = (r_a + 63) / 64;              // 64-rank blocks in use
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(B.full + 8u * i, 1);
@@ -486,11 +469,38 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (threadIdx.x == 0) {
+    prefetch_map(&mx);
+    prefetch_map(UP ? &mB : &mA);
+    if (a.Co > 0) prefetch_map(UP ? &mA : &mB);
+    if (a.Co > 0 && a.base) prefetch_map(&mbase);
+  }
+  pdl_wait();
+  pdl_launch_dependents();  // everything before this kernel is complete
+  if (blockIdx.x == 0 && warp == kTcWorkers + 1)
+    lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
+  const LoraTile tile = lora_find_tile<kTcRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
+  const int r_a = tile.found ? lora_rank(a.ranks, tile.adapter, a.L, a.R) : 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_arrive();  // barriers are initialised in every CTA before any remote arrival (the workers wait)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + G::tmem_off);
+  if (r_a == 0) {  // the whole cluster: no such tile, or one without a contribution
+    if (warp == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(G::TM_COLS) : "memory");
+    if (tile.found) lora_copy_rows(a, tile, rank, CS, kTcThreads);
+    return;
+  }
+  const int r16 = (r_a + 15) & ~15;
+  // Steps down and up: the cluster's CTAs take the 64-column chunks of a row in
+  // turn, so that at any time they read and write neighbouring pieces of it.
+  const int D = ((a.Ci + 63) / 64 - rank + CS - 1) / CS, U = ((a.Co + 63) / 64 - rank + CS - 1) / CS;
+  const bool drop = a.drop.thr != 0;
+  const bool pad = (r_a & 15) != 0;                 // the last k-step of the up product needs zeros
+  const bool patch = pad || (UP == 0 && drop);     // workers touch the slots before the MMA
+  const int blocks = (r_a + 63) / 64;              // 64-rank blocks in use
+
+  cluster_arrive();  // barriers are initialised in every CTA before any remote arrival (the workers wait)
   const uint32_t t_smem = sbase + NS * G::SLOT;
 
   if (warp == 0) {
@@ -695,7 +705,7 @@ BQ_DEV bool wgrad_next(WgradRows &w, const WgradArgs &a, int adapter, int rank) 
         const int s = w.s0 + lane;
         bool hit = false;
         w.len = 0;
-        if (s < a.S && a.seg_adapter[s] == adapter) {
+        if (s < a.S && __ldcg(a.seg_adapter + s) == adapter) {
           w.len = lora_segment(a.seg_off, s, a.M, &w.start);
           hit = w.len > 0;
         }
@@ -812,6 +822,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (threadIdx.x == 0 && a.S > 0) prefetch_map(map);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -889,13 +900,14 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     const int wt = (int)threadIdx.x - 64;
     const DropState dst = drop_state(a.drop);
     bool ok = true;
+    if (!is_b) pdl_wait();  // dt is complete; all else was before the kernel that makes it began
     auto load_p = [&](float4 (&pv)[G::PPT], int row0, int rows) {
 #pragma unroll
       for (int k = 0; k < G::PPT; ++k) {
         const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
         pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (m < rows && r < r_a) {
-          pv[k] = *reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r);
+          pv[k] = __ldcg(reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r));
           if (r + 1 >= r_a) pv[k].y = 0.0f;
           if (r + 2 >= r_a) pv[k].z = 0.0f;
           if (r + 3 >= r_a) pv[k].w = 0.0f;
@@ -983,6 +995,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
   }
 
   // ---- the sums meet: every CTA's ring is idle, it holds the sums now --------
+  pdl_wait();  // no CTA leaves before the kernel that makes dt is complete
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
