@@ -863,6 +863,7 @@ bq_status linear_any(const void *x, bq_dtype xtype, int64_t M, int64_t K, const 
 namespace {
 
 constexpr int64_t kMaxRows = 1ll << 30, kMaxCols = 1ll << 28;
+constexpr int kTcDeepCS = 2;  // clusters at least this large, one CTA per SM, beat two CTAs per SM
 
 // thr = round(p 65536); false where p is no probability below 1 - 2^-17.
 bool drop_args(double p, const uint64_t *rng, DropArgs *d) {
@@ -968,25 +969,36 @@ int64_t cluster_places(int cs, int per_sm) {
 }
 
 // Long segments: 128-row tiles on tcgen05.
-template <int XT, int UP, int RP>
-bq_status launch_lora_tc(LoraArgs a, cudaStream_t st) {
-  using G = TcGeom<RP>;
+template <int XT, int UP, int RP, bool DEEP>
+bq_status launch_lora_tc(LoraArgs a, int64_t tiles, int cs, cudaStream_t st) {
+  using G = TcGeom<RP, DEEP>;
   CUtensorMap mx = {}, mA = {}, mB = {}, mbase = {};
   const int64_t K = UP ? a.Co : a.Ci, N = UP ? a.Ci : a.Co;
   if (!make_map(&mx, a.x, XT == 1, a.Ci, a.M, 0, a.ldx, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
   if (K && !make_map(&mA, a.A, XT == 1, K, a.R, a.L, K, (int64_t)a.R * K, 64, (a.R + 15) & ~15)) return BQ_ERR_CUDA;
   if (N && !make_map(&mB, a.B, XT == 1, a.R, N, a.L, a.R, (int64_t)a.R * N, 64, 64)) return BQ_ERR_CUDA;
   if (a.base && a.Co && !make_map(&mbase, a.base, XT == 1, a.Co, a.M, 0, a.ldbase, 0, 64, kTcXBox)) return BQ_ERR_CUDA;
-  constexpr auto kern = lora_tc_kernel<XT, UP, RP>;
+  constexpr auto kern = lora_tc_kernel<XT, UP, RP, DEEP>;
   if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
+  a.CS = cs;
+  return launch_cluster(kern, tiles * cs, cs, G::THREADS, G::total, overlap_mode() >= 1, st, mx, mA, mB, mbase, a);
+}
+
+template <int XT, int UP>
+bq_status launch_lora_long(const LoraArgs &a, cudaStream_t st) {
   // The largest cluster with which all tiles are on the GPU at once: with one
   // tile more than places the last one takes as long as all the others (72
   // tiles in clusters of 4: 114 us, in clusters of 3: 88 us).
   const int64_t tiles = lora_tiles(a, kTcRows);
-  int cs = kTcMaxCS;
-  while (cs > 1 && cluster_places(cs, RP == 64 ? 2 : 1) < tiles) --cs;
-  a.CS = cs;
-  return launch_cluster(kern, tiles * cs, cs, kTcThreads, G::total, overlap_mode() >= 1, st, mx, mA, mB, mbase, a);
+  const auto fit = [&](int per_sm) {
+    int cs = kTcMaxCS;
+    while (cs > 1 && cluster_places(cs, per_sm) < tiles) --cs;
+    return cs;
+  };
+  const int one = fit(1);
+  if (a.R > 64) return launch_lora_tc<XT, UP, 128, true>(a, tiles, one, st);
+  if (one >= kTcDeepCS) return launch_lora_tc<XT, UP, 64, true>(a, tiles, one, st);
+  return launch_lora_tc<XT, UP, 64, false>(a, tiles, fit(2), st);
 }
 
 template <int XT, int UP>
@@ -997,7 +1009,7 @@ bq_status launch_lora(const LoraArgs &a, cudaStream_t st) {
     if (a.R <= 16) return launch_lora_t<XT, UP, 16>(a, st);
     return a.R <= 64 ? launch_lora_t<XT, UP, 64>(a, st) : launch_lora_t<XT, UP, 128>(a, st);
   }
-  return a.R <= 64 ? launch_lora_tc<XT, UP, 64>(a, st) : launch_lora_tc<XT, UP, 128>(a, st);
+  return launch_lora_long<XT, UP>(a, st);
 }
 
 struct WgradInputs {

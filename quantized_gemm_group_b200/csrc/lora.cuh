@@ -126,22 +126,33 @@ BQ_DEV void lora_check_segments(const int *seg_off, const int *seg_adapter, cons
 }
 
 // Rows without a contribution: base's (nothing to do in place), t zero.  The
-// cluster's warps take a row each in turn, eight loads in flight a lane.
-BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int rank, int CS, int threads) {
-  const int lane = threadIdx.x & 31, warps = threads >> 5;
+// cluster's warps take a row each in turn; a lane has eight loads in flight
+// while it stores the eight before.
+BQ_DEV void lora_copy_load(uint4 (&v)[8], const uint16_t *from, int c, int n) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    v[k] = (from && c + 256 * k < n) ? ld_stream_v4(from + c + 256 * k) : make_uint4(0, 0, 0, 0);
+}
+BQ_DEV void lora_copy_store(const uint4 (&v)[8], uint16_t *to, int c, int n) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (c + 256 * k < n) st_v4(to + c + 256 * k, v[k]);
+}
+__device__ __noinline__ void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int rank, int CS, int threads) {
+  const int lane = threadIdx.x & 31, warps = threads >> 5, n = a.Co;
   for (int m = rank * warps + (threadIdx.x >> 5); m < tile.rows; m += CS * warps) {
     const int64_t row = tile.row0 + m;
-    if (a.base != a.y) {
-      const uint16_t *from = a.base + row * a.ldbase;
+    if (a.base != a.y && n > 0) {
+      const uint16_t *from = a.base ? a.base + row * a.ldbase : nullptr;
       uint16_t *to = a.y + row * a.ldy;
-      for (int c = 8 * lane; c < a.Co; c += 8 * 256) {
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[k] = (a.base && c + 256 * k < a.Co) ? *reinterpret_cast<const uint4 *>(from + c + 256 * k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + 256 * k < a.Co) st_v4(to + c + 256 * k, v[k]);
+      uint4 v[8], w[8];
+      int c = 8 * lane;
+      lora_copy_load(v, from, c, n);
+      for (; c < n; c += 2 * 2048) {
+        lora_copy_load(w, from, c + 2048, n);
+        lora_copy_store(v, to, c, n);
+        lora_copy_load(v, from, c + 2 * 2048, n);
+        lora_copy_store(w, to, c + 2048, n);
       }
     }
     if (a.t)

@@ -8,16 +8,19 @@
 // of 4096 -> 14336 510 us).  Here tiles come by TMA, tcgen05.mma reads them from shared
 // memory, and threads touch only t, the masks and the output.
 //
-// lora_tc_kernel: a cluster of 8 CTAs owns 128 rows of one segment.  Each
-// contracts an eighth of the columns into tensor memory (down), sends its
-// partial sums to the CTA that owns the row (16 rows each, distributed shared
-// memory, added in rank order: the same bits every time), the owner sends the
-// 16-bit parts of t to all eight, and each writes an eighth of the output
-// columns (up).  Two CTAs fit an SM, so one's exchange hides behind the
-// other's streams.  Roles (10 warps): warp 0 producer (one ring of slots: a
-// chunk of x and of the down pool, later a chunk of base and of the up pool);
-// warp 1 issues tcgen05.mma; warps 2-9 (two per TMEM lane quadrant) mask x,
-// exchange the sums and finish the output.
+// lora_tc_kernel: a cluster of up to 8 CTAs owns 128 rows of one segment.  Each
+// contracts its share of the columns into tensor memory (down), sends its
+// partial sums to the CTA that owns the row (distributed shared memory, added
+// in rank order: the same bits every time), the owner sends the 16-bit parts of
+// t to all of them, and each writes its share of the output columns (up).
+// Roles (10 or 18 warps): warp 0 producer (one ring of slots: a chunk of x and
+// of the down pool, later a chunk of base and of the up pool); warp 1 issues
+// tcgen05.mma; the others (two or four per TMEM lane quadrant) mask x, exchange
+// the sums and finish the output.
+// Two persistent kernels instead (down, then up, one CTA per SM, equal runs of
+// steps, sums through global scratch) took 92 us where this one takes 80, and
+// 43 where it takes 33 (4096 rows, 4096 -> 4096, rank 64): a second launch and
+// the sums' way through L2 cost more than the exchange.
 //
 // Rounding: t enters the up product as two 16-bit parts, t = hi + lo (bf16:
 // relative error below 2^-17; fp16: the row is first scaled by a power of two so
@@ -40,8 +43,6 @@
 namespace bq {
 
 constexpr int kTcRows = 128;                   // rows per tile (MMA M)
-constexpr int kTcWorkers = 8;                  // worker warps
-constexpr int kTcThreads = 32 * (2 + kTcWorkers);
 constexpr int kTcXBox = 64;                    // rows per TMA box of x and base
 constexpr int kTcMaxCS = 8;                    // CTAs per cluster at most
 
@@ -158,11 +159,19 @@ BQ_DEV float2 tc_scale(float m) {
 // forward / input gradient
 // ---------------------------------------------------------------------------
 
-template <int RP> struct TcGeom {
+// DEEP: one CTA per SM with a deep ring and 16 worker warps, for grids that do
+// not fill the GPU twice (and for ranks above 64, whose pools are twice as
+// large); else two CTAs per SM, so that one's exchange hides behind the other's
+// streams.
+template <int RP, bool DEEP> struct TcGeom {
+  static_assert(DEEP || RP == 64, "two CTAs of rank 128 do not fit an SM");
+  static constexpr int NG = DEEP ? 4 : 2;           // worker warps per TMEM lane quadrant
+  static constexpr int WORKERS = 4 * NG;            // worker warps
+  static constexpr int THREADS = 32 * (2 + WORKERS);
   static constexpr int X_BYTES = kTcRows * 128;     // 128 rows x 64 columns
   static constexpr int W_BYTES = RP * 128;          // 64 x RP of a pool
   static constexpr int SLOT = X_BYTES + W_BYTES;
-  static constexpr int NS = (RP == 64) ? 3 : 4;     // two CTAs per SM / one
+  static constexpr int NS = RP == 128 ? 4 : DEEP ? 7 : 3;
   static constexpr int BLOCKS = RP / 64;            // 64-rank blocks
   static constexpr int T_BYTES = 2 * BLOCKS * kTcRows * 128;  // hi and lo
   // the sums' buffer lies there before: [CS][ceil(128 / CS) rows][RP] fp32, at most 133 rows
@@ -170,28 +179,28 @@ template <int RP> struct TcGeom {
   static_assert(T_AREA >= T_BYTES, "t and the sums share their place");
   static constexpr int TOTAL0 = NS * SLOT + T_AREA;
   static constexpr int bar_off = TOTAL0;
-  static constexpr int nbar = 4 * NS + 10;
+  static constexpr int nbar = 4 * NS + 2 * NG + 6;
   static constexpr int scale_off = bar_off + 8 * nbar;  // fp32 per row
   static constexpr int tmem_off = scale_off + 4 * kTcRows;
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
-  static constexpr int TM_COLS = 256;               // P: RP columns, output: 2 x 64
-  static constexpr int PER_THREAD = kTcRows * RP / 4 / (32 * kTcWorkers);  // quads of sums per worker, CS = 1
+  static constexpr int TM_COLS = DEEP ? 512 : 256;  // P: RP columns, output: NG x 64
+  static constexpr int PER_THREAD = kTcRows * RP / 4 / (32 * WORKERS);  // quads of sums per worker, CS = 1
 };
 
 struct TcBars {
   uint32_t full, masked, free_mma, free_out;  // [NS]
-  uint32_t p_full, d_full, d_empty;           // 1, [2], [2]
+  uint32_t p_full, d_full, d_empty;           // 1, [ng], [ng]
   uint32_t recv, taken, t_in, t_ready, done;
-  BQ_DEV TcBars(uint32_t base, int ns) {
+  BQ_DEV TcBars(uint32_t base, int ns, int ng) {
     full = base;
     masked = full + 8u * ns;
     free_mma = masked + 8u * ns;
     free_out = free_mma + 8u * ns;
     p_full = free_out + 8u * ns;
     d_full = p_full + 8u;
-    d_empty = d_full + 16u;
-    recv = d_empty + 16u;
+    d_empty = d_full + 8u * ng;
+    recv = d_empty + 8u * ng;
     taken = recv + 8u;
     t_in = taken + 8u;
     t_ready = t_in + 8u;
@@ -199,15 +208,15 @@ struct TcBars {
   }
 };
 
-// Worker warps (two per TMEM lane quadrant, thread = row of the tile).
-template <int XT, int UP, int RP>
+// Worker warps (NG per TMEM lane quadrant, thread = row of the tile).
+template <int XT, int UP, int RP, bool DEEP>
 BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, int r16, int D, int U, bool patch, bool pad,
                             int rank, uint32_t tmem, uint32_t sbase, unsigned char *smem, const TcBars &B, volatile int *abort, cg::cluster_group &cluster) {
   const int CS = a.CS;
-  using G = TcGeom<RP>;
+  using G = TcGeom<RP, DEEP>;
   constexpr int NS = G::NS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = (int)threadIdx.x - 64;
-  const int quad = warp & 3, half = (warp - 2) >> 2, m = quad * 32 + lane;
+  const int quad = warp & 3, grp = (warp - 2) >> 2, m = quad * 32 + lane;
   const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
   const bool drop = a.drop.thr != 0;
   const DropState dst = drop_state(a.drop);
@@ -218,12 +227,12 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   if (patch)
     for (int s = 0; s < D && ok; ++s) {
       const int slot = s % NS;
-      constexpr int PT = kTcRows * 8 / (32 * kTcWorkers);  // 16-byte chunks per worker
+      constexpr int PT = kTcRows * 8 / (32 * G::WORKERS);  // 16-byte chunks per worker
       uint4 mask[PT];
       if (UP == 0 && drop) {
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
-          const int i = wt + k * 32 * kTcWorkers;
+          const int i = wt + k * 32 * G::WORKERS;
           mask[k] = drop_mask8(drop_block(dst, (uint32_t)(8 * (rank + CS * s) + (i & 7)), (uint32_t)(tile.row0 + (i >> 3))),
                                dst.thr_hi);
         }
@@ -234,7 +243,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
         const uint32_t xs = sbase + slot * G::SLOT;
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
-          const int i = wt + k * 32 * kTcWorkers, row = i >> 3;
+          const int i = wt + k * 32 * G::WORKERS, row = i >> 3;
           const uint32_t at = xs + row * 128 + (((i & 7) ^ (row & 7)) << 4);
           sts_v4(at, and4(lds_v4(at), mask[k]));
         }
@@ -257,7 +266,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   if (ok) {
     const int rr = rank * own + m % own;
     float *to = cluster.map_shared_rank(recv, m / own) + rr * RP;
-    for (int cgp = half; cgp < r16 / 16; cgp += 2) {
+    for (int cgp = grp; cgp < r16 / 16; cgp += G::NG) {
       float v[16];
       if (D > 0) {
         tmem_ld16(tmem + lane_addr + cgp * 16, v);
@@ -280,7 +289,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     const float pre = (UP == 0) ? a.drop.inv_keep : sc;  // to t (or dt) as stored
 #pragma unroll
     for (int k = 0; k < G::PER_THREAD; ++k) {
-      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), chunk = i % (RP / 4), r = 4 * chunk;
+      const int i = wt + k * 32 * G::WORKERS, ml = i / (RP / 4), chunk = i % (RP / 4), r = 4 * chunk;
       const int row = rank * own + ml;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (ml < own && row < tile.rows && r < r_a)
@@ -306,8 +315,8 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     const float post = (UP == 0) ? a.scales[tile.adapter] : 1.0f;  // to what the up step multiplies
 #pragma unroll
     for (int k = 0; k < G::PER_THREAD; ++k) {
-      const int i = wt + k * 32 * kTcWorkers, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * own + ml;
-      if (k * 32 * kTcWorkers >= own * (RP / 4)) break;
+      const int i = wt + k * 32 * G::WORKERS, ml = i / (RP / 4), r = 4 * (i % (RP / 4)), row = rank * own + ml;
+      if (k * 32 * G::WORKERS >= own * (RP / 4)) break;
       float2 sc = make_float2(1.0f, 1.0f);
       if (XT == 0) {
         float mx = fmaxf(fmaxf(fabsf(sum[k][0] * post), fabsf(sum[k][1] * post)),
@@ -338,12 +347,12 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   }
 
   // ---- up: base + t W2, 64 columns a step -------------------------------------
-  // The two warps of a quadrant take alternate steps (each its own buffer of
-  // tensor memory), so that one's waits hide behind the other's work: a step
-  // is a chain of waits, and with both warps on the same step it took 1.3 us.
+  // The warps of a quadrant take steps in turn (each its own buffer of tensor
+  // memory), so that one's waits hide behind the others' work: a step is a
+  // chain of waits, and with both warps of two on the same step it took 1.3 us.
   const float row_scale = (XT == 0 && ok) ? *reinterpret_cast<const float *>(smem + G::scale_off + 4 * m) : 1.0f;
   uint16_t *out = a.y + (int64_t)(tile.row0 + quad * 32 + (lane >> 3)) * a.ldy + 8 * (lane & 7);
-  for (int j = half; j < U && ok; j += 2) {
+  for (int j = grp; j < U && ok; j += G::NG) {
     const int s = D + j, slot = s % NS;
     const uint32_t xs = sbase + slot * G::SLOT, ws = xs + G::X_BYTES;
     const int col0 = 64 * (rank + CS * j);
@@ -365,19 +374,19 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
       if (pad && UP == 1 && wg < 8 * (r16 - r_a)) sts_v4(ws + (r_a + (wg >> 3)) * 128 + (wg & 7) * 16, make_uint4(0, 0, 0, 0));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane < 2) mbar_arrive(B.masked + 8u * slot);  // for the quadrant's other warp too
+      if (lane < G::NG) mbar_arrive(B.masked + 8u * slot);  // for the quadrant's other warps too
     }
-    ok = vote(mbar_wait(B.d_full + 8u * half, (j >> 1) & 1));
+    ok = vote(mbar_wait(B.d_full + 8u * grp, (j / G::NG) & 1));
     if (!ok) break;
     tc_fence_after();
 #pragma unroll
     for (int hc = 0; hc < 2; ++hc) {
       uint32_t d[32];
-      tmem_ld32(tmem + lane_addr + RP + 64 * half + 32 * hc, d);
+      tmem_ld32(tmem + lane_addr + RP + 64 * grp + 32 * hc, d);
       if (hc == 1) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B.d_empty + 8u * half);
+        if (lane == 0) mbar_arrive(B.d_empty + 8u * grp);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -427,11 +436,11 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
 // mbase: base [M, Co].
 // Registers are handed out for whole groups of four warps, so two CTAs of 10
 // warps fit an SM as two of 12 do.
-template <int XT, int UP, int RP>
-__global__ void __launch_bounds__(RP == 64 ? 384 : kTcThreads, RP == 64 ? 2 : 1)
+template <int XT, int UP, int RP, bool DEEP>
+__global__ void __launch_bounds__(DEEP ? TcGeom<RP, DEEP>::THREADS : 384, DEEP ? 1 : 2)
 lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mA,
                const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mbase, const LoraArgs a) {
-  using G = TcGeom<RP>;
+  using G = TcGeom<RP, DEEP>;
   constexpr int NS = G::NS;
   extern __shared__ __align__(1024) unsigned char tsm_raw[];
   const uint32_t raw = smem_u32(tsm_raw);
@@ -441,24 +450,24 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int CS = a.CS, rank = (int)blockIdx.x % CS, tile_index = (int)blockIdx.x / CS;
   volatile int *abort = reinterpret_cast<volatile int *>(smem + G::abort_off);
-  const TcBars B(sbase + G::bar_off, NS);
+  const TcBars B(sbase + G::bar_off, NS, G::NG);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(B.full + 8u * i, 1);
-      mbar_init(B.masked + 8u * i, kTcWorkers);
+      mbar_init(B.masked + 8u * i, G::WORKERS);
       mbar_init(B.free_mma + 8u * i, 1);
-      mbar_init(B.free_out + 8u * i, kTcWorkers / 2);
+      mbar_init(B.free_out + 8u * i, 4);
     }
     mbar_init(B.p_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < G::NG; ++i) {
       mbar_init(B.d_full + 8u * i, 1);
-      mbar_init(B.d_empty + 8u * i, kTcWorkers / 2);
+      mbar_init(B.d_empty + 8u * i, 4);
     }
-    mbar_init(B.recv, CS * kTcWorkers);
-    mbar_init(B.taken, CS * kTcWorkers);
-    mbar_init(B.t_in, CS * kTcWorkers);
-    mbar_init(B.t_ready, kTcWorkers);
+    mbar_init(B.recv, CS * G::WORKERS);
+    mbar_init(B.taken, CS * G::WORKERS);
+    mbar_init(B.t_in, CS * G::WORKERS);
+    mbar_init(B.t_ready, G::WORKERS);
     mbar_init(B.done, 1);
     *abort = 0;
     mbar_fence_init();
@@ -477,7 +486,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   }
   pdl_wait();
   pdl_launch_dependents();  // everything before this kernel is complete
-  if (blockIdx.x == 0 && warp == kTcWorkers + 1)
+  if (blockIdx.x == 0 && warp == G::WORKERS + 1)
     lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
   const LoraTile tile = lora_find_tile<kTcRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
   const int r_a = tile.found ? lora_rank(a.ranks, tile.adapter, a.L, a.R) : 0;
@@ -488,7 +497,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   if (r_a == 0) {  // the whole cluster: no such tile, or one without a contribution
     if (warp == 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(G::TM_COLS) : "memory");
-    if (tile.found) lora_copy_rows(a, tile, rank, CS, kTcThreads);
+    if (tile.found) lora_copy_rows(a, tile, rank, CS, G::THREADS);
     return;
   }
   const int r16 = (r_a + 15) & ~15;
@@ -496,7 +505,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   // turn, so that at any time they read and write neighbouring pieces of it.
   const int D = ((a.Ci + 63) / 64 - rank + CS - 1) / CS, U = ((a.Co + 63) / 64 - rank + CS - 1) / CS;
   const bool drop = a.drop.thr != 0;
-  const bool pad = (r_a & 15) != 0;                 // the last k-step of the up product needs zeros
+  // the last k-step of the up product needs zeros behind the rank (behind R there are)
+  const bool pad = (r_a & 15) != 0 && r_a < a.R;
   const bool patch = pad || (UP == 0 && drop);     // workers touch the slots before the MMA
   const int blocks = (r_a + 63) / 64;              // 64-rank blocks in use
 
@@ -582,8 +592,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
       const int ks = r16 / 16;
       if (ok && U > 0) ok = mbar_wait(B.t_ready, 0);
       for (int j = 0; j < U && ok; ++j) {
-        const int buf = j & 1;
-        ok = mbar_wait(ready + 8u * slot, use) && (j < 2 || mbar_wait(B.d_empty + 8u * buf, ((j >> 1) & 1) ^ 1));
+        const int buf = j % G::NG;
+        ok = mbar_wait(ready + 8u * slot, use) && (j < G::NG || mbar_wait(B.d_empty + 8u * buf, ((j / G::NG) & 1) ^ 1));
         if (!ok) break;
         tc_fence_after();
         const uint64_t wd = wd0 + (uint64_t)(slot * (G::SLOT >> 4));
@@ -605,7 +615,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     __syncwarp();
     cluster_wait();
   } else {
-    lora_tc_workers<XT, UP, RP>(a, tile, r_a, r16, D, U, patch, pad, rank, tmem, sbase, smem, B, abort, cluster);
+    lora_tc_workers<XT, UP, RP, DEEP>(a, tile, r_a, r16, D, U, patch, pad, rank, tmem, sbase, smem, B, abort, cluster);
   }
 
   // everything issued by this CTA has finished before the tensor memory goes
