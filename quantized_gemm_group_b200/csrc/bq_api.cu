@@ -947,9 +947,11 @@ template <int XT, int UP, int RP>
 bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
   using G = LoraGeom<16, RP>;
   const int64_t tiles = lora_tiles(a, 16);
-  // CTAs per tile: as many as keep the grid within a few waves
+  // CTAs per tile (a power of two: each owns an equal share of the sums): as many
+  // as keep the grid within two CTAs per SM (with six, 64 requests took 15.2 us
+  // instead of 10.9 and 128 of rank 64 42.6 instead of 35.7)
   int cs = 8;
-  while (cs > 1 && tiles * cs > 6 * (int64_t)sm_count()) cs /= 2;
+  while (cs > 1 && tiles * cs > 2 * (int64_t)sm_count()) cs /= 2;
   a.CS = cs;
   a.slice_c = (int)round_up((a.Ci + cs - 1) / cs, G::SC);
   a.slice_o = (int)round_up((a.Co + cs - 1) / cs, 32);

@@ -138,13 +138,15 @@ BQ_DEV void lora_copy_store(const uint4 (&v)[8], uint16_t *to, int c, int n) {
   for (int k = 0; k < 8; ++k)
     if (c + 256 * k < n) st_v4(to + c + 256 * k, v[k]);
 }
-__device__ __noinline__ void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int rank, int CS, int threads) {
-  const int lane = threadIdx.x & 31, warps = threads >> 5, n = a.Co;
-  for (int m = rank * warps + (threadIdx.x >> 5); m < tile.rows; m += CS * warps) {
-    const int64_t row = tile.row0 + m;
-    if (a.base != a.y && n > 0) {
-      const uint16_t *from = a.base ? a.base + row * a.ldbase : nullptr;
-      uint16_t *to = a.y + row * a.ldy;
+// (Not inlined, and without the kernel's argument struct: it is rarely run, and
+// the struct's address would put a copy of it on every thread's stack.)
+__device__ __noinline__ void lora_copy_some(const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy, float *t, int n,
+                                            int R, int first, int rows, int step) {
+  const int lane = threadIdx.x & 31;
+  for (int m = first; m < rows; m += step) {
+    if (base != y && n > 0) {
+      const uint16_t *from = base ? base + m * ldbase : nullptr;
+      uint16_t *to = y + m * ldy;
       uint4 v[8], w[8];
       int c = 8 * lane;
       lora_copy_load(v, from, c, n);
@@ -155,9 +157,17 @@ __device__ __noinline__ void lora_copy_rows(const LoraArgs &a, const LoraTile &t
         lora_copy_store(w, to, c + 2048, n);
       }
     }
-    if (a.t)
-      for (int i = lane; i < a.R; i += 32) a.t[row * a.R + i] = 0.0f;
+    if (t)
+      for (int i = lane; i < R; i += 32) t[(int64_t)m * R + i] = 0.0f;
   }
+}
+BQ_DEV void lora_copy_rows(const LoraArgs &a, const LoraTile &tile, int rank, int CS, int threads) {
+  const int warps = threads >> 5;
+  const int64_t row = tile.row0;
+  const bool copy = a.base != a.y;
+  lora_copy_some(a.base ? a.base + row * a.ldbase : nullptr, a.ldbase, copy ? a.y + row * a.ldy : nullptr, a.ldy,
+                 a.t ? a.t + row * a.R : nullptr, copy ? a.Co : 0, a.R, rank * warps + (int)(threadIdx.x >> 5), tile.rows,
+                 CS * warps);
 }
 
 // The rank to use: 0 (no contribution) without an adapter or with a bad one.
