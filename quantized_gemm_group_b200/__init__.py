@@ -2,7 +2,7 @@
 
 The compute lives in ``libbq.so`` (CUDA kernels behind the C ABI of
 ``include/bq.h``); ``bq`` is its thin ctypes binding and ``synth`` the seeded
-input generators.  Importing the package does not load the library; the first
+input generators; ``adapters`` runs the linear layer with low-rank adapters.  Importing the package does not load the library; the first
 ``bq`` call does, and raises if it is missing.
 """
-__all__ = ["bq", "synth", "build"]
+__all__ = ["bq", "synth", "build", "adapters"]
