@@ -313,6 +313,14 @@ def _device(name: str, v) -> int:
     return dev
 
 
+def _empty(shape, like, stream):
+    """A result of like's type and device that belongs to the stream that the kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
 def _launch(name: str, fn, dev: int, stream, *args):
     """Call fn on the tensors' device, on its current stream or the one given."""
     if dev != torch._C._cuda_getDevice():
@@ -329,7 +337,7 @@ def bq_dropout(x: torch.Tensor, p: float, rng=None, out=None, stream=None):
     rows, cols = x.shape
     dev, dtype = _device("x", x), x.dtype
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=x.device)
+        out = _empty((rows, cols), x, stream)
     _launch("bq_dropout", lib().bq_dropout, dev, stream, x.data_ptr(), DTYPE_CODE[dtype], rows, cols,
             _matrix("x", x, rows, cols, dtype, dev), p, _rng_ptr(rng, dev), out.data_ptr(),
             _matrix("out", out, rows, cols, dtype, dev))
@@ -349,7 +357,7 @@ def bq_lora(x: torch.Tensor, A, B, ranks, scales, seg_off, seg_adapter, base=Non
     S, = seg_adapter.shape
     dev, dtype = _device("x", x), x.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x.device)
+        out = _empty((M, N), x, stream)
     args = _LORA_ARGS.pack(
         x.data_ptr(), _dense("A", A, (L, R, K), dtype, dev), _dense("B", B, (L, N, R), dtype, dev),
         _dense("ranks", ranks, (L,), torch.int32, dev), _dense("scales", scales, (L,), torch.float32, dev),

@@ -393,6 +393,20 @@ def test_two_streams_at_once(lens):
             assert torch.equal(a, b)
 
 
+def test_results_belong_to_the_stream():
+    """A result allocated for another stream is not memory that the current stream's kernels may still use."""
+    c = Case(520, 264, 64, [64, 33], [3, 9], [0, 1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for call, cols in ((lambda: c.forward(stream=s), c.N), (lambda: bq.bq_dropout(c.x, 0.5, c.rng, stream=s), c.K)):
+        old = torch.empty((c.M, cols), dtype=c.dtype, device=DEV)
+        at = old.data_ptr()
+        del old
+        out = call()
+        assert out.data_ptr() != at
+        torch.cuda.synchronize()
+
+
 def test_offsets_past_32_bits():
     """Rows so far apart that element offsets pass 2^31, with both kernels."""
     for lens in ([2, 3], [120, 50]):
