@@ -369,7 +369,7 @@ typedef struct {
     const float *scales;
     const int32_t *seg_off, *seg_adapter;
     const uint64_t *rng;         /* dropout on x, as in bq_dropout; NULL allowed when p rounds to 0 */
-    const void *base;            /* [M, N] of dtype, row stride ldbase; NULL: zeros.  May be y. */
+    const void *base;            /* [M, N] of dtype, row stride ldbase; NULL: zeros.  May be y (ldbase = ldy). */
     void *y;                     /* [M, N] of dtype, row stride ldy */
     float *t;                    /* NULL, or fp32 [M, R], 16-byte aligned: receives t for bq_lora_grad */
     int64_t M, K, N, ldx, ldbase, ldy;
@@ -387,7 +387,7 @@ typedef struct {
     const float *scales;
     const int32_t *seg_off, *seg_adapter;
     const uint64_t *rng;         /* the forward's, unchanged */
-    const void *base;            /* [M, K] added to dx, row stride ldbase; NULL: zeros.  May be dx. */
+    const void *base;            /* [M, K] added to dx, row stride ldbase; NULL: zeros.  May be dx (ldbase = lddx). */
     void *dx;                    /* [M, K] of dtype, row stride lddx; NULL: not wanted */
     float *dt;                   /* fp32 [M, R] scratch, needed for dx and dA; holds dt afterwards */
     float *dA, *dB;              /* fp32 [L, R, K], [L, N, R]; NULL: not wanted */

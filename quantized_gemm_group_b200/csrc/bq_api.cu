@@ -1090,6 +1090,7 @@ bq_status bq_lora(const bq_lora_args *args, void *stream) {
   if ((s = lora_matrix(q.x, M, K, q.ldx)) != BQ_OK) return s;
   if ((s = lora_matrix(q.y, M, N, q.ldy)) != BQ_OK) return s;
   if (q.base && (s = lora_matrix(q.base, M, N, q.ldbase)) != BQ_OK) return s;
+  if (q.base && q.base == q.y && M > 1 && q.ldbase != q.ldy) return BQ_ERR_SHAPE;  // in place means the same rows
   if ((s = lora_matrix(q.A, q.L, K, K)) != BQ_OK || (s = lora_matrix(q.B, q.L, N, N)) != BQ_OK) return s;
   if (!q.seg_off || !q.seg_adapter || (q.L && (!q.ranks || !q.scales)) || (a.drop.thr && !q.rng)) return BQ_ERR_NULL;
   if (!aligned(q.seg_off, 4) || !aligned(q.seg_adapter, 4) || !aligned(q.ranks, 4) || !aligned(q.scales, 4) ||
@@ -1135,6 +1136,7 @@ bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
     if (q.dA && (s = lora_matrix(q.x, M, K, q.ldx)) != BQ_OK) return s;
     if (q.dx && (s = lora_matrix(q.dx, M, K, q.lddx)) != BQ_OK) return s;
     if (q.dx && q.base && (s = lora_matrix(q.base, M, K, q.ldbase)) != BQ_OK) return s;
+    if (q.dx && q.base == q.dx && M > 1 && q.ldbase != q.lddx) return BQ_ERR_SHAPE;
     if (q.dx && (s = lora_matrix(q.A, L, K, K)) != BQ_OK) return s;
     if (need_dt && (s = lora_matrix(q.B, L, N, N)) != BQ_OK) return s;
     if (!q.seg_off || !q.seg_adapter || (need_dt && !q.dt) || (q.dB && !q.t) || (a.drop.thr && !q.rng)) return BQ_ERR_NULL;

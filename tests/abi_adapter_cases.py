@@ -97,3 +97,8 @@ def test_grad(L):
     assert grad(L, lddy=76) == bq.BQ_ERR_SHAPE
     assert grad(L, M=0, dA=0, dB=0) == bq.BQ_OK               # no rows and no gradients of weights wanted
     assert grad(L, L=0, M=0) == bq.BQ_OK                      # no adapters: empty gradients
+
+
+def test_in_place_means_the_same_rows(L):
+    assert forward(L, ldbase=80) == bq.BQ_ERR_SHAPE
+    assert grad(L, ldbase=80) == bq.BQ_ERR_SHAPE
