@@ -945,17 +945,17 @@ int64_t lora_tiles(const LoraArgs &a, int bm) {
 // Short segments: 16-row tiles on mma.sync.
 template <int XT, int UP, int RP>
 bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
-  using G = LoraGeom<16, RP>;
-  const int64_t tiles = lora_tiles(a, 16);
+  using G = LoraGeom<UP, RP>;
+  const int64_t tiles = lora_tiles(a, kLoraRows);
   // CTAs per tile (a power of two: each owns an equal share of the sums): as many
-  // as keep the grid within two CTAs per SM (with six, 64 requests took 15.2 us
-  // instead of 10.9 and 128 of rank 64 42.6 instead of 35.7)
+  // as keep the grid within two CTAs per SM (with six, 64 requests took 15.7 us
+  // instead of 10.8 and 128 of rank 64 35.8 instead of 29.3)
   int cs = 8;
   while (cs > 1 && tiles * cs > 2 * (int64_t)sm_count()) cs /= 2;
   a.CS = cs;
   a.slice_c = (int)round_up((a.Ci + cs - 1) / cs, G::SC);
   a.slice_o = (int)round_up((a.Co + cs - 1) / cs, 32);
-  constexpr auto kern = lora_kernel<XT, UP, 16, RP>;
+  constexpr auto kern = lora_kernel<XT, UP, RP>;
   if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
   return launch_cluster(kern, tiles * cs, cs, kLoraThreads, G::TOTAL, overlap_mode() >= 1, st, a);
 }
@@ -1187,7 +1187,8 @@ bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
   w.S = rows ? S : 0;
   w.drop = a.drop;
   const WgradInputs in = {q.x, q.dy, M == 1 ? K : q.ldx, M == 1 ? N : q.lddy};
-  // launched over the kernel that makes dt (dB's part does not wait for it)
+  // launched over the kernel that makes dt whatever BQ_OPT_LINEAR_OVERLAP says: both are
+  // this call's, and dA's part waits for it (dB's does not read dt)
   const bool after_dt = rows && need_dt;
   if (dtype == BQ_BF16) return R <= 64 ? launch_wgrad<1, 64>(w, in, after_dt, st) : launch_wgrad<1, 128>(w, in, after_dt, st);
   return R <= 64 ? launch_wgrad<0, 64>(w, in, after_dt, st) : launch_wgrad<0, 128>(w, in, after_dt, st);

@@ -7,33 +7,41 @@
 // pool comes first and in how its elements lie: A is [L, R, K] (contiguous
 // along the contraction of the forward's down step), B is [L, N, R].
 //
-// Bound: memory.  x and base are read once and y written once; with r <= 64
-// the products cost less than the traffic on mma.sync, so that the tensor
-// memory path would gain nothing here.
+// This file's kernel takes short segments (up to 24 rows each on average),
+// where the pools are most of the traffic; lora_tc.cuh takes longer ones.
+// Bound: memory and, below 16 rows, the latency of the chain x -> t -> y.
+// On mma.sync a warp works on its own and starts with the first bytes; 16 rows
+// would leave 112 of the 128 rows of a tensor memory tile empty.
 //
-// Split: a cluster of CS CTAs owns a tile of BM rows of one segment.  Each CTA
-// contracts its share of the columns (down), the partial [BM, R] sums meet in
-// distributed shared memory (added in rank order: no atomics, the same bits
-// every time), and each CTA then writes its share of the output columns (up).
-// t never goes through global memory (the training forward stores it once for
-// the backward pass), and one launch does the whole adapter.  The grid has
-// one cluster for each tile that S segments of M rows can need; a cluster
-// finds its segment by a prefix sum over the segment lengths, so lengths stay
-// on the device.
+// Split: a cluster of CS CTAs owns 16 rows of one segment.  Each CTA contracts
+// its share of the columns (down), the partial [16, R] sums meet in distributed
+// shared memory (added in rank order: no atomics, the same bits every time),
+// and each CTA then writes its share of the output columns (up).  t never goes
+// through global memory (the training forward stores it once for the backward
+// pass), and one launch does the whole adapter.  The grid has one cluster for
+// each tile that S segments of M rows can need; a cluster finds its segment by
+// a prefix sum over the segment lengths, so lengths stay on the device.
 //
-// Down: a warp takes 16 MT rows and every KQ-th run of 32 columns.  A lane's
-// 16-byte load of a row (8 consecutive columns) is used as the fragments of
-// two k-steps: the contraction may run in any order as long as both operands
-// use the same one, so x needs no shared memory and dropout is applied to the
-// loaded registers, one generator block a load.  The pool goes through a
-// cp.async ring shared by the row groups.
+// Down: a warp takes every eighth run of 32 columns.  A lane's 16-byte load of
+// a row (8 consecutive columns) is used as the fragments of two k-steps: the
+// contraction may run in any order as long as both operands use the same one,
+// so x needs no shared memory and dropout is applied to the loaded registers,
+// one generator block a load.  The pool goes through a cp.async ring.
 // Up: t (fp32) is split into two bf16 parts t = hi + lo (relative error below
 // 2^-17; one bf16 would lose 2^-9 of it), two mma.sync a step.  fp16
 // pools are split into two bf16 parts as well (11 bits = 8 + 3, exact): t does
 // not have fp16's range.  A warp takes 32 output columns of the tile; the
 // column that fragment slot n of tile j stands for is 8 (n / 2) + 2 j + n % 2,
 // so that a lane ends with 8 consecutive columns: base and y move as 16-byte
-// vectors straight from and to registers.
+// vectors.
+//
+// Measured (bf16, each request its own adapter, 4096 columns in): 1 token to
+// 4096 columns, rank 16 5.5 us; 16 requests to 28672, rank 16 14 us and to
+// 14336, rank 64 18 us; 128 requests to 4096, rank 64 29 us (134 MB of pools:
+// 71 % of the copy rate); 256 requests to 14336, rank 64 (64 adapters) 89 us.
+// Few requests are bound by the chain of waits and by the warps' instructions
+// (16 requests: one issued every 2.7 cycles by two warps a scheduler; sixteen
+// warps a CTA were slower, as clusters of 8 then find 15 places instead of 33).
 #pragma once
 #include <cooperative_groups.h>
 
@@ -46,6 +54,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr int kLoraRows = 16;  // rows per tile
 
 struct LoraArgs {
   const uint16_t *x;      // [M, Ci] rows of stride ldx: x, or dy
@@ -181,6 +190,12 @@ BQ_DEV void cp_async16(uint32_t dst, const void *src, bool valid) {
   const int n = valid ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+BQ_DEV void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+BQ_DEV void cp_async8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 BQ_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> BQ_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -229,21 +244,27 @@ template <int XT> BQ_DEV void pool_parts(uint32_t w, uint32_t &hi, uint32_t &lo)
   }
 }
 
-// Tile geometry for BM rows and the padded rank RP.
-template <int BM, int RP> struct LoraGeom {
-  static constexpr int MT = (BM == 16 || RP == 128) ? 1 : 2;  // 16-row tiles per warp (down)
-  static constexpr int RG = BM / (16 * MT);                   // row groups
-  static constexpr int KQ = kLoraWarps / RG;                  // warps sharing a step's columns
-  static constexpr int SC = 32 * KQ;                          // columns per step
-  static constexpr int NST = (BM == 16 && RP == 128) ? 2 : 3;
+// Tile geometry for the padded rank RP.  Shared memory holds, one after the
+// other, the down ring; the warps' partial sums (from 0); t (from 0), the up
+// pool's staging (UP = 1) and the up ring (to MAIN); the owned sums from MAIN.
+constexpr int lora_max(int a, int b) { return a > b ? a : b; }
+template <int UP, int RP> struct LoraGeom {
+  static constexpr int SC = 32 * kLoraWarps;                  // columns per step
+  static constexpr int NST = RP == 128 ? 2 : 3;
   static constexpr int STAGE = RP * SC * 2;                   // pool bytes per stage
-  static constexpr int PARTIAL = KQ * BM * RP * 4;            // the warps' partial sums
-  static constexpr int T_BYTES = 2 * BM * RP * 2;             // t as two bf16 parts
+  static constexpr int PARTIAL = kLoraWarps * kLoraRows * RP * 4;  // the warps' partial sums
+  static constexpr int T_BYTES = 2 * kLoraRows * RP * 2;      // t as two bf16 parts
   static constexpr int WT_BYTES = RP * 64;                    // a warp's 32 columns of A (UP = 1)
-  static constexpr int MAIN0 = (NST * STAGE > PARTIAL) ? NST * STAGE : PARTIAL;
-  static constexpr int UPB = T_BYTES + kLoraWarps * WT_BYTES;
-  static constexpr int MAIN = (MAIN0 > UPB) ? MAIN0 : UPB;
-  static constexpr int RECV = BM * RP * 4;
+  // the up ring (UP = 0): a warp's 32 columns of base and B for two turns, stage 0
+  // last (four turns: the same within 3 %)
+  static constexpr int DU = UP == 1 ? 0 : 2;
+  static constexpr int SLOT = UP == 1 ? 0 : kLoraRows * 64 + RP * 64;
+  static constexpr int UP_STAGE = kLoraWarps * SLOT;
+  static constexpr int LOW = T_BYTES + (UP == 0 ? 0 : kLoraWarps * WT_BYTES);
+  static constexpr int MAIN = lora_max(lora_max(NST * STAGE, LOW + DU * UP_STAGE), lora_max(PARTIAL, LOW) + UP_STAGE);
+  static constexpr int CLEAR = UP == 1 ? 0 : (MAIN - PARTIAL) / lora_max(UP_STAGE, 1);
+  static constexpr int EARLY = CLEAR < DU ? CLEAR : DU;  // stages clear of the sums
+  static constexpr int RECV = kLoraRows * RP * 4;
   static constexpr int TOTAL = MAIN + RECV;
 };
 
@@ -253,19 +274,16 @@ template <int BM, int RP> struct LoraGeom {
 // 8 i + {0, 1} of one transposed fragment are read together.
 template <int UP, int RP, int SC> BQ_DEV uint32_t down_offset(int r, int c) {
   if (UP == 0) return (uint32_t)(r * SC * 2 + ((c ^ ((r & 1) << 2)) << 4));
-  int f;
-  if (RP >= 64) f = (((r >> 3) & 3) << 1) | (r & 1);
-  else if (RP == 32) f = (r >> 3) & 3;
-  else f = (r >> 3) & 1;
+  const int f = RP >= 64 ? (((r >> 3) & 3) << 1) | (r & 1) : (r >> 3) & 1;
   return (uint32_t)(r * RP * 2 + ((c ^ f) << 4));
 }
 
 // grid = CS x tiles, cluster = (CS, 1, 1).
-template <int XT, int UP, int BM, int RP>
+template <int XT, int UP, int RP>
 __global__ void __launch_bounds__(kLoraThreads, (RP == 128 || (XT == 0 && RP == 64)) ? 1 : 2)
 lora_kernel(LoraArgs a) {
-  using G = LoraGeom<BM, RP>;
-  constexpr int MT = G::MT, RG = G::RG, KQ = G::KQ, SC = G::SC, NST = G::NST;
+  using G = LoraGeom<UP, RP>;
+  constexpr int SC = G::SC, NST = G::NST;
   constexpr int NT = RP / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
@@ -277,7 +295,7 @@ lora_kernel(LoraArgs a) {
   pdl_launch_dependents();  // everything before this kernel is complete
   if (blockIdx.x == 0 && warp == kLoraWarps - 1)
     lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
-  const LoraTile tile = lora_find_tile<BM>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
+  const LoraTile tile = lora_find_tile<kLoraRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
   if (!tile.found) return;  // the whole cluster
   const int r_a = lora_rank(a.ranks, tile.adapter, a.L, a.R);
   const int o_begin = rank * a.slice_o, o_end = min(a.Co, o_begin + a.slice_o);
@@ -299,26 +317,21 @@ lora_kernel(LoraArgs a) {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // ---- down: partial sums of this warp's rows over its columns -------------
-  const int rg = warp % RG, kq = warp / RG;
   const int steps = (c_end > c_begin) ? (c_end - c_begin + SC - 1) / SC : 0;
-  const uint16_t *xrow[MT][2];
-  bool xval[MT][2];
+  const uint16_t *xrow[2];
+  bool xval[2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = (rg * MT + mt) * 16 + h * 8 + g;
-      xval[mt][h] = m < tile.rows;
-      xrow[mt][h] = a.x + (int64_t)(tile.row0 + (xval[mt][h] ? m : 0)) * a.ldx;
-    }
-  const int lane_c = 32 * kq + 8 * t4;
-  auto load_x = [&](uint4 (&v)[MT][2], int step) {
+  for (int h = 0; h < 2; ++h) {
+    const int m = h * 8 + g;
+    xval[h] = m < tile.rows;
+    xrow[h] = a.x + (int64_t)(tile.row0 + (xval[h] ? m : 0)) * a.ldx;
+  }
+  const int lane_c = 32 * warp + 8 * t4;
+  auto load_x = [&](uint4 (&v)[2], int step) {
     const int c = c_begin + step * SC + lane_c;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[mt][h] = (step < steps && c < c_end && xval[mt][h]) ? ld_stream_v4(xrow[mt][h] + c) : make_uint4(0, 0, 0, 0);
+    for (int h = 0; h < 2; ++h)
+      v[h] = (step < steps && c < c_end && xval[h]) ? ld_stream_v4(xrow[h] + c) : make_uint4(0, 0, 0, 0);
   };
   auto load_pool = [&](int step) {
     if (step < steps) {
@@ -342,19 +355,17 @@ lora_kernel(LoraArgs a) {
     cp_async_commit();
   };
 
-  float acc[MT][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
 
-  uint4 xv[2][MT][2];
+  uint4 xv[2][2];
   load_x(xv[0], 0);
 #pragma unroll
   for (int s = 0; s < NST - 1; ++s) load_pool(s);
-  auto run_step = [&](uint4 (&cur)[MT][2], uint4 (&nxt)[MT][2], int step) {
+  auto run_step = [&](uint4 (&cur)[2], uint4 (&nxt)[2], int step) {
     load_x(nxt, step + 1);
     cp_async_wait<NST - 2>();
     __syncthreads();  // the stage is visible, and the one read last step is free
@@ -362,45 +373,28 @@ lora_kernel(LoraArgs a) {
     if (UP == 0 && drop) {
       const int c = c_begin + step * SC + lane_c;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int m = (rg * MT + mt) * 16 + h * 8 + g;
-          const uint4 k = drop_mask8(drop_block(dst, (uint32_t)c >> 3, (uint32_t)(tile.row0 + m)), dst.thr_hi);
-          cur[mt][h].x &= k.x;
-          cur[mt][h].y &= k.y;
-          cur[mt][h].z &= k.z;
-          cur[mt][h].w &= k.w;
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint4 k = drop_mask8(drop_block(dst, (uint32_t)c >> 3, (uint32_t)(tile.row0 + h * 8 + g)), dst.thr_hi);
+        cur[h].x &= k.x;
+        cur[h].y &= k.y;
+        cur[h].z &= k.z;
+        cur[h].w &= k.w;
+      }
     }
     const uint32_t stage = sbase + (step % NST) * G::STAGE;
-    uint32_t fa[MT][2][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      fa[mt][0][0] = cur[mt][0].x;
-      fa[mt][0][1] = cur[mt][1].x;
-      fa[mt][0][2] = cur[mt][0].y;
-      fa[mt][0][3] = cur[mt][1].y;
-      fa[mt][1][0] = cur[mt][0].z;
-      fa[mt][1][1] = cur[mt][1].z;
-      fa[mt][1][2] = cur[mt][0].w;
-      fa[mt][1][3] = cur[mt][1].w;
-    }
+    const uint32_t fa[2][4] = {{cur[0].x, cur[1].x, cur[0].y, cur[1].y}, {cur[0].z, cur[1].z, cur[0].w, cur[1].w}};
     if (UP == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         if (nt < nt_used) {
-          const uint4 w = lds_v4(stage + down_offset<UP, RP, SC>(nt * 8 + g, 4 * kq + t4));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            MmaT<XT>::mma(acc[mt][nt], fa[mt][0], w.x, w.y);
-            MmaT<XT>::mma(acc[mt][nt], fa[mt][1], w.z, w.w);
-          }
+          const uint4 w = lds_v4(stage + down_offset<UP, RP, SC>(nt * 8 + g, 4 * warp + t4));
+          MmaT<XT>::mma(acc[nt], fa[0], w.x, w.y);
+          MmaT<XT>::mma(acc[nt], fa[1], w.z, w.w);
         }
     } else {
       // lane i addresses row i % 8 of matrix i / 8: (nt, low), (nt, high), (nt + 1, low), (nt + 1, high)
       const int j = lane & 7, hi = (lane >> 3) & 1, nx = lane >> 4;
-      const int row = 32 * kq + 8 * (j >> 1) + (j & 1) + 2 * hi;
+      const int row = 32 * warp + 8 * (j >> 1) + (j & 1) + 2 * hi;
 #pragma unroll
       for (int nt = 0; nt < NT; nt += 2)
         if (nt < nt_used) {
@@ -408,11 +402,8 @@ lora_kernel(LoraArgs a) {
           for (int ks = 0; ks < 2; ++ks) {
             uint32_t w[4];
             ldmatrix_x4_trans(w, stage + down_offset<UP, RP, SC>(row + 4 * ks, nt + nx));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              MmaT<XT>::mma(acc[mt][nt], fa[mt][ks], w[0], w[1]);
-              MmaT<XT>::mma(acc[mt][nt + 1], fa[mt][ks], w[2], w[3]);
-            }
+            MmaT<XT>::mma(acc[nt], fa[ks], w[0], w[1]);
+            MmaT<XT>::mma(acc[nt + 1], fa[ks], w[2], w[3]);
           }
         }
     }
@@ -425,24 +416,25 @@ lora_kernel(LoraArgs a) {
   __syncthreads();
 
   // ---- the sums meet: warps in this CTA's memory, CTAs in their owner's ----
-  float *part = reinterpret_cast<float *>(smem);  // [KQ][BM][RP]
+  float *part = reinterpret_cast<float *>(smem);  // [kLoraWarps][16][RP]
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int m = (rg * MT + mt) * 16 + g;
-      float *p = part + ((kq * BM + m) * RP + nt * 8 + 2 * t4);
-      *reinterpret_cast<float2 *>(p) = make_float2(acc[mt][nt][0], acc[mt][nt][1]);
-      *reinterpret_cast<float2 *>(p + 8 * RP) = make_float2(acc[mt][nt][2], acc[mt][nt][3]);
-    }
+  for (int nt = 0; nt < NT; ++nt) {
+    float *p = part + ((warp * kLoraRows + g) * RP + nt * 8 + 2 * t4);
+    *reinterpret_cast<float2 *>(p) = make_float2(acc[nt][0], acc[nt][1]);
+    *reinterpret_cast<float2 *>(p + 8 * RP) = make_float2(acc[nt][2], acc[nt][3]);
+  }
   // ---- up: this CTA's output columns, 32 per warp and turn -----------------
-  // A turn's pool elements are asked for a turn ahead (the first ones before the
-  // sums are exchanged): a turn is shorter than the way to L2 and back.
-  constexpr int MTU = BM / 16;             // 16-row tiles
+  // UP = 0: a turn's elements of B and base are asked for two turns ahead (the
+  // first before the sums are exchanged), as a turn is shorter than the way to
+  // memory and back.  A lane copies what it reads itself, so no warp waits for
+  // another (through registers, B one turn ahead and base none: 16 requests to
+  // 14336 columns, rank 64 23.6 us instead of 18, 1536 rows in 64 segments 48
+  // instead of 37).  UP = 1 goes through registers: A's columns are transposed
+  // on the way.
   constexpr int KC = (RP >= 32) ? RP / 32 : 1;  // runs of 32 ranks (one of 16 where RP = 16)
   constexpr int KS = (RP >= 32) ? 2 : 1;   // k-steps in a run
   constexpr int PER = 4 * KS;              // UP = 0: ranks that a lane holds of a run
-  constexpr int NV = (RP >= 32) ? RP / 8 : (UP == 0 ? 4 : 2);  // vectors per lane and turn
+  constexpr int NV = (RP >= 32) ? RP / 8 : 2;  // UP = 1: vectors per lane and turn
   const int w_rows = (RP >= 32) ? (r_a + 31) & ~31 : 16;       // UP = 1: rows of A to stage
   // UP = 1: the row of A in vector k of this lane; the eight rows of one store
   // instruction lie in different banks
@@ -455,44 +447,56 @@ lora_kernel(LoraArgs a) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) wv[k] = make_uint4(0, 0, 0, 0);
     if (cb >= o_end) return;
-    if (UP == 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = cb + 8 * (g >> 1) + 2 * j + (g & 1);
-        const uint16_t *p = poolB + (int64_t)n * a.R;
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-          const int r = 32 * i + PER * t4;
-          if (n < o_end && r < r_a) {
-            if (KS == 2) {
-              wv[j * KC + i] = ld_nc_v4(p + r);
-            } else {
-              const uint2 q = *reinterpret_cast<const uint2 *>(p + r);
-              wv[j * KC + i].x = q.x;
-              wv[j * KC + i].y = q.y;
-            }
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int r = w_row(k), c = cb + 8 * (lane & 3);
-        if (r < r_a && c < o_end) wv[k] = ld_nc_v4(poolA + (int64_t)r * K + c);
-      }
+    for (int k = 0; k < NV; ++k) {
+      const int r = w_row(k), c = cb + 8 * (lane & 3);
+      if (r < r_a && c < o_end) wv[k] = ld_nc_v4(poolA + (int64_t)r * K + c);
     }
   };
-  load_w(o_begin + 32 * warp);
+  constexpr int DU = UP == 0 ? G::DU : 1;
+  auto up_stage = [&](int turn) { return sbase + G::MAIN - (turn % DU + 1) * G::UP_STAGE + warp * G::SLOT; };
+  // What no copy fills is never used: rows behind the tile and columns behind the
+  // slice are not stored, ranks behind r_a are masked.
+  const int row_a = tile.row0 + g, first = o_begin + 32 * warp;
+  const bool in0 = g < tile.rows, in1 = g + 8 < tile.rows;
+  const uint16_t *wp = poolB + (int64_t)(first + 8 * (g >> 1) + (g & 1)) * a.R + PER * t4;
+  const uint16_t *bp = a.base + row_a * a.ldbase + first + 8 * t4;
+  int next = first;  // column of the next turn to ask for
+  auto fetch = [&](int turn) {
+    const uint32_t at = up_stage(turn) + lane * 16;
+    if (a.base && next + 8 * t4 < o_end) {
+      if (in0) cp_async16(at, bp);
+      if (in1) cp_async16(at + 512, bp + 8 * a.ldbase);
+    }
+    if (next + 8 * (g >> 1) < o_end) {
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
+        if (32 * i + PER * t4 < r_a) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (KS == 2) cp_async16(at + 1024 + (j * KC + i) * 512, wp + 2 * j * a.R + 32 * i);
+            else cp_async8(at + 1024 + j * 256 - lane * 8, wp + 2 * j * a.R);
+          }
+        }
+    }
+    cp_async_commit();
+    next += 32 * kLoraWarps;
+    bp += 32 * kLoraWarps;
+    wp += 32 * kLoraWarps * a.R;
+  };
+  if (UP == 1) load_w(o_begin + 32 * warp);
+#pragma unroll
+  for (int i = 0; i < G::EARLY; ++i) fetch(i);
 
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  const int per = BM * RP / CS;  // elements that one CTA owns
+  const int per = kLoraRows * RP / CS;  // elements that one CTA owns
   float *recv = reinterpret_cast<float *>(smem + G::MAIN);  // [CS][per]
-  for (int e = 4 * (int)threadIdx.x; e < BM * RP; e += 4 * kLoraThreads) {
+  for (int e = 4 * (int)threadIdx.x; e < kLoraRows * RP; e += 4 * kLoraThreads) {
     float4 s = *reinterpret_cast<const float4 *>(part + e);
 #pragma unroll
-    for (int q = 1; q < KQ; ++q) {
-      const float4 v = *reinterpret_cast<const float4 *>(part + q * BM * RP + e);
+    for (int q = 1; q < kLoraWarps; ++q) {
+      const float4 v = *reinterpret_cast<const float4 *>(part + q * kLoraRows * RP + e);
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
@@ -502,6 +506,8 @@ lora_kernel(LoraArgs a) {
     *reinterpret_cast<float4 *>(cluster.map_shared_rank(recv, owner) + rank * per + (e - owner * per)) = s;
   }
   cluster.sync();
+#pragma unroll
+  for (int i = G::EARLY; i < G::DU; ++i) fetch(i);
   {
     const float sc = a.scales[tile.adapter];
     const float pre = (UP == 0) ? a.drop.inv_keep : sc;  // to t (or dt) as stored
@@ -529,7 +535,7 @@ lora_kernel(LoraArgs a) {
       for (int q = 0; q < CS; ++q) {
         uint8_t *tt = cluster.map_shared_rank(smem, q);
         *reinterpret_cast<uint2 *>(tt + at) = hi;
-        *reinterpret_cast<uint2 *>(tt + BM * RP * 2 + at) = lo;
+        *reinterpret_cast<uint2 *>(tt + kLoraRows * RP * 2 + at) = lo;
       }
     }
   }
@@ -537,14 +543,28 @@ lora_kernel(LoraArgs a) {
 
   const uint32_t tbase = sbase, wbase = sbase + G::T_BYTES + warp * G::WT_BYTES;
   const float out_scale = (UP == 1) ? a.drop.inv_keep : 1.0f;
-  for (int cb = o_begin + 32 * warp; cb < o_end; cb += 32 * kLoraWarps) {
+  int turn = 0;
+  for (int cb = o_begin + 32 * warp; cb < o_end; cb += 32 * kLoraWarps, ++turn) {
+    const uint32_t from = up_stage(turn) + lane * 16;
+    if (UP == 0) cp_async_wait<DU - 1>();
     uint32_t w[4][KC][KS][2];  // fragments of the up pool: n-tile, run, k-step
     if (UP == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
-          uint32_t v[4] = {wv[j * KC + i].x, wv[j * KC + i].y, wv[j * KC + i].z, wv[j * KC + i].w};
+          uint32_t v[4];
+          if (KS == 2) {
+            const uint4 q = lds_v4(from + 1024 + (j * KC + i) * 512);
+            v[0] = q.x;
+            v[1] = q.y;
+            v[2] = q.z;
+            v[3] = q.w;
+          } else {
+            const uint2 q = lds_v2(from + 1024 + j * 256 - lane * 8);
+            v[0] = q.x;
+            v[1] = q.y;
+          }
           const int left = r_a - (32 * i + PER * t4);
           if (left < PER)  // what lies behind the rank may be anything
 #pragma unroll
@@ -591,86 +611,83 @@ lora_kernel(LoraArgs a) {
           }
         }
     }
-    load_w(cb + 32 * kLoraWarps);
+    if (UP == 1) load_w(cb + 32 * kLoraWarps);
     const int col = cb + 8 * t4;
+    const bool ok0 = in0 && col < o_end, ok1 = in1 && col < o_end;
+    uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+    if (UP == 1 && a.base) {
+      if (ok0) b0 = *reinterpret_cast<const uint4 *>(a.base + row_a * a.ldbase + col);
+      if (ok1) b1 = *reinterpret_cast<const uint4 *>(a.base + (row_a + 8) * a.ldbase + col);
+    }
+    float d[4][4];
 #pragma unroll
-    for (int mt = 0; mt < MTU; ++mt) {
-      if (mt * 16 >= tile.rows) break;
-      const int m0 = mt * 16 + g, m1 = m0 + 8;
-      const bool ok0 = m0 < tile.rows && col < o_end, ok1 = m1 < tile.rows && col < o_end;
-      uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-      if (a.base) {
-        if (ok0) b0 = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m0) * a.ldbase + col);
-        if (ok1) b1 = *reinterpret_cast<const uint4 *>(a.base + (tile.row0 + m1) * a.ldbase + col);
-      }
-      float d[4][4];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+    for (int i = 0; i < KC; ++i) {
+      if (32 * i >= r_a) break;
+      uint32_t fh[KS][4], fl[KS][4];
 #pragma unroll
-      for (int i = 0; i < KC; ++i) {
-        if (32 * i >= r_a) break;
-        uint32_t fh[KS][4], fl[KS][4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // rows g, g + 8
-          const int m = mt * 16 + half * 8 + g;
-          if (KS == 2) {
-            int c = 4 * i + t4;
-            if (RP >= 64) c ^= (m & 1) << 2;
-            const uint32_t at = tbase + m * RP * 2 + c * 16;
-            const uint4 h = lds_v4(at), l = lds_v4(at + BM * RP * 2);
-            fh[0][half] = h.x;
-            fh[0][2 + half] = h.y;
-            fh[KS - 1][half] = h.z;
-            fh[KS - 1][2 + half] = h.w;
-            fl[0][half] = l.x;
-            fl[0][2 + half] = l.y;
-            fl[KS - 1][half] = l.z;
-            fl[KS - 1][2 + half] = l.w;
-          } else {
-            const uint32_t at = tbase + m * RP * 2 + t4 * 8;
-            const uint2 h = lds_v2(at), l = lds_v2(at + BM * RP * 2);
-            fh[0][half] = h.x;
-            fh[0][2 + half] = h.y;
-            fl[0][half] = l.x;
-            fl[0][2 + half] = l.y;
-          }
+      for (int half = 0; half < 2; ++half) {  // rows g, g + 8
+        const int m = half * 8 + g;
+        if (KS == 2) {
+          int c = 4 * i + t4;
+          if (RP >= 64) c ^= (m & 1) << 2;
+          const uint32_t at = tbase + m * RP * 2 + c * 16;
+          const uint4 h = lds_v4(at), l = lds_v4(at + kLoraRows * RP * 2);
+          fh[0][half] = h.x;
+          fh[0][2 + half] = h.y;
+          fh[KS - 1][half] = h.z;
+          fh[KS - 1][2 + half] = h.w;
+          fl[0][half] = l.x;
+          fl[0][2 + half] = l.y;
+          fl[KS - 1][half] = l.z;
+          fl[KS - 1][2 + half] = l.w;
+        } else {
+          const uint32_t at = tbase + m * RP * 2 + t4 * 8;
+          const uint2 h = lds_v2(at), l = lds_v2(at + kLoraRows * RP * 2);
+          fh[0][half] = h.x;
+          fh[0][2 + half] = h.y;
+          fl[0][half] = l.x;
+          fl[0][2 + half] = l.y;
         }
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t h0, l0, h1, l1;
-            pool_parts<XT>(w[j][i][ks][0], h0, l0);
-            pool_parts<XT>(w[j][i][ks][1], h1, l1);
-            MmaT<1>::mma(d[j], fh[ks], h0, h1);
-            MmaT<1>::mma(d[j], fl[ks], h0, h1);
-            if (XT == 0) MmaT<1>::mma(d[j], fh[ks], l0, l1);
-          }
       }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int m = half ? m1 : m0;
-        if (!(half ? ok1 : ok0)) continue;
-        const uint4 b = half ? b1 : b0;
-        uint32_t bw[4] = {b.x, b.y, b.z, b.w}, ow[4];
-        uint4 keep = make_uint4(0, 0, 0, 0);
-        if (UP == 1 && drop) keep = drop_block(dst, (uint32_t)col >> 3, (uint32_t)(tile.row0 + m));
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v0 = d[j][2 * half], v1 = d[j][2 * half + 1];
-          if (UP == 1 && drop) {
-            v0 = drop_keep(keep, 2 * j, dst.thr_hi) ? v0 * out_scale : 0.0f;
-            v1 = drop_keep(keep, 2 * j + 1, dst.thr_hi) ? v1 * out_scale : 0.0f;
-          }
-          const float2 bf = Elem<XT>::pair(bw[j]);
-          ow[j] = (uint32_t)Elem<XT>::from_float(bf.x + v0) | ((uint32_t)Elem<XT>::from_float(bf.y + v1) << 16);
+          uint32_t h0, l0, h1, l1;
+          pool_parts<XT>(w[j][i][ks][0], h0, l0);
+          pool_parts<XT>(w[j][i][ks][1], h1, l1);
+          MmaT<1>::mma(d[j], fh[ks], h0, h1);
+          MmaT<1>::mma(d[j], fl[ks], h0, h1);
+          if (XT == 0) MmaT<1>::mma(d[j], fh[ks], l0, l1);
         }
-        *reinterpret_cast<uint4 *>(a.y + (tile.row0 + m) * a.ldy + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-      }
     }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!(half ? ok1 : ok0)) continue;
+      uint4 b = half ? b1 : b0;
+      if (UP == 0 && a.base) b = lds_v4(from + 512 * half);
+      uint32_t bw[4] = {b.x, b.y, b.z, b.w}, ow[4];
+      uint4 keep = make_uint4(0, 0, 0, 0);
+      if (UP == 1 && drop) keep = drop_block(dst, (uint32_t)col >> 3, (uint32_t)(row_a + 8 * half));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v0 = d[j][2 * half], v1 = d[j][2 * half + 1];
+        if (UP == 1 && drop) {
+          v0 = drop_keep(keep, 2 * j, dst.thr_hi) ? v0 * out_scale : 0.0f;
+          v1 = drop_keep(keep, 2 * j + 1, dst.thr_hi) ? v1 * out_scale : 0.0f;
+        }
+        const float2 bf = Elem<XT>::pair(bw[j]);
+        ow[j] = (uint32_t)Elem<XT>::from_float(bf.x + v0) | ((uint32_t)Elem<XT>::from_float(bf.y + v1) << 16);
+      }
+      *reinterpret_cast<uint4 *>(a.y + (row_a + 8 * half) * a.ldy + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+    }
+    if (UP == 0) fetch(turn + DU);  // this turn's stage has been read
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace bq

@@ -26,6 +26,9 @@
 // relative error below 2^-17; fp16: the row is first scaled by a power of two so
 // that its largest value lies in [2^14, 2^15), error below 2^-22 of it).  One
 // part would lose 2^-9; the second costs a matrix instruction and no traffic.
+// The accumulators are fp32, but the tensor core rounds them towards zero: a sum
+// of n steps is off by up to n 2^-23 of its largest partial sum (measured: dA of
+// 8192 rows over 14336 columns 1e-5, dB 2.5e-6 of their norms).
 //
 // What lies outside never enters a product: columns behind K, N or R are
 // zero-filled by TMA (the pools are 3D maps, so an adapter's end is an edge),
@@ -485,7 +488,6 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
     if (a.Co > 0 && a.base) prefetch_map(&mbase);
   }
   pdl_wait();
-  pdl_launch_dependents();  // everything before this kernel is complete
   if (blockIdx.x == 0 && warp == G::WORKERS + 1)
     lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
   const LoraTile tile = lora_find_tile<kTcRows>(a.seg_off, a.seg_adapter, a.S, a.M, tile_index);
@@ -493,6 +495,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // everything before this kernel is complete, and this CTA has its tensor memory
+  pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + G::tmem_off);
   if (r_a == 0) {  // the whole cluster: no such tile, or one without a contribution
     if (warp == 1)
