@@ -26,9 +26,8 @@
 // relative error below 2^-17; fp16: the row is first scaled by a power of two so
 // that its largest value lies in [2^14, 2^15), error below 2^-22 of it).  One
 // part would lose 2^-9; the second costs a matrix instruction and no traffic.
-// The accumulators are fp32, but the tensor core rounds them towards zero: a sum
-// of n steps is off by up to n 2^-23 of its largest partial sum (measured: dA of
-// 8192 rows over 14336 columns 1e-5, dB 2.5e-6 of their norms).
+// The accumulators are fp32; the roundings of their many steps add up (measured:
+// dA of 8192 rows, dt over 14336 columns, 1e-5 of its norm, dB 2.5e-6).
 //
 // What lies outside never enters a product: columns behind K, N or R are
 // zero-filled by TMA (the pools are 3D maps, so an adapter's end is an edge),
