@@ -26,8 +26,7 @@
 // relative error below 2^-17; fp16: the row is first scaled by a power of two so
 // that its largest value lies in [2^14, 2^15), error below 2^-22 of it).  One
 // part would lose 2^-9; the second costs a matrix instruction and no traffic.
-// The accumulators are fp32; the roundings of their many steps add up (measured:
-// dA of 8192 rows, dt over 14336 columns, 1e-5 of its norm, dB 2.5e-6).
+// Long sums leave the tensor core's accumulator every 16 instructions (kTcRun).
 //
 // What lies outside never enters a product: columns behind K, N or R are
 // zero-filled by TMA (the pools are 3D maps, so an adapter's end is an edge),
@@ -47,6 +46,13 @@ namespace bq {
 constexpr int kTcRows = 128;                   // rows per tile (MMA M)
 constexpr int kTcXBox = 64;                    // rows per TMA box of x and base
 constexpr int kTcMaxCS = 8;                    // CTAs per cluster at most
+// Steps down whose products add up in tensor memory: 16 instructions.  The
+// accumulator cuts where fp32 additions round (up to 2^-23 of the running sum
+// lost at each instruction, always towards zero), so a run this long loses about
+// 3e-7 and the runs are added in registers.  In one run 14336 columns in clusters
+// of 2 (448 instructions) lost 8e-6 of t's norm, in single CTAs 1.6e-5; plain fp32
+// products lose about 1e-6.
+constexpr int kTcRun = 4;
 
 // ---------------------------------------------------------------------------
 // primitives
@@ -181,18 +187,22 @@ template <int RP, bool DEEP> struct TcGeom {
   static_assert(T_AREA >= T_BYTES, "t and the sums share their place");
   static constexpr int TOTAL0 = NS * SLOT + T_AREA;
   static constexpr int bar_off = TOTAL0;
-  static constexpr int nbar = 4 * NS + 2 * NG + 6;
+  static constexpr int nbar = 4 * NS + 2 * NG + 9;
   static constexpr int scale_off = bar_off + 8 * nbar;  // fp32 per row
   static constexpr int tmem_off = scale_off + 4 * kTcRows;
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
-  static constexpr int TM_COLS = DEEP ? 512 : 256;  // P: RP columns, output: NG x 64
+  static constexpr int D_COL = 2 * RP;              // output: NG x 64 columns behind the two buffers of P
+  static constexpr int TM_COLS = DEEP ? 512 : 256;
+  static_assert(D_COL + 64 * NG <= TM_COLS, "tensor memory");
+  static constexpr int P_GROUPS = RP / 16 / NG;     // groups of 16 ranks whose sums a worker warp keeps
   static constexpr int PER_THREAD = kTcRows * RP / 4 / (32 * WORKERS);  // quads of sums per worker, CS = 1
 };
 
 struct TcBars {
   uint32_t full, masked, free_mma, free_out;  // [NS]
-  uint32_t p_full, d_full, d_empty;           // 1, [ng], [ng]
+  uint32_t p_full, p_empty;                   // [2]
+  uint32_t d_full, d_empty;                   // [ng]
   uint32_t recv, taken, t_in, t_ready, done;
   BQ_DEV TcBars(uint32_t base, int ns, int ng) {
     full = base;
@@ -200,7 +210,8 @@ struct TcBars {
     free_mma = masked + 8u * ns;
     free_out = free_mma + 8u * ns;
     p_full = free_out + 8u * ns;
-    d_full = p_full + 8u;
+    p_empty = p_full + 16u;
+    d_full = p_empty + 16u;
     d_empty = d_full + 8u * ng;
     recv = d_empty + 8u * ng;
     taken = recv + 8u;
@@ -224,6 +235,36 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   const DropState dst = drop_state(a.drop);
   bool ok = true;
   auto vote = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+
+  // A finished run of the down product is added to this warp's sums: row m,
+  // ranks 16 (grp + NG k) onwards.
+  float psum[G::P_GROUPS][16];
+#pragma unroll
+  for (int k = 0; k < G::P_GROUPS; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) psum[k][i] = 0.0f;
+  const int runs = (D + kTcRun - 1) / kTcRun;
+  int run = 0;
+  auto add_run = [&]() {
+    const int buf = run & 1;
+    ok = vote(!*abort && mbar_wait(B.p_full + 8u * buf, (run >> 1) & 1));
+    if (!ok) return;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < G::P_GROUPS; ++k) {
+      const int cgp = grp + G::NG * k;
+      if (cgp < r16 / 16) {
+        float v[16];
+        tmem_ld16(tmem + lane_addr + buf * RP + cgp * 16, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) psum[k][i] += v[i];
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(B.p_empty + 8u * buf);
+    ++run;
+  };
 
   // ---- down: masks on x (drawn while x is on its way) -----------------------
   if (patch)
@@ -253,6 +294,9 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(B.masked + 8u * slot);
+      // the run before this one: by now its products are done, and its buffer is
+      // free before the next run asks for it
+      if (s % kTcRun == kTcRun - 2 && s >= kTcRun) add_run();
     }
 
   // ---- the sums meet -------------------------------------------------------
@@ -260,26 +304,20 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
   // chunks XORed with the row so that a warp's rows lie in different banks
   const int own = (kTcRows + CS - 1) / CS;
   float *recv = reinterpret_cast<float *>(smem + NS * G::SLOT);
-  if (ok && D > 0) {
-    ok = vote(mbar_wait(B.p_full, 0));
-    tc_fence_after();
-  }
+  while (ok && run < runs) add_run();
   cluster_wait();
   if (ok) {
     const int rr = rank * own + m % own;
     float *to = cluster.map_shared_rank(recv, m / own) + rr * RP;
-    for (int cgp = grp; cgp < r16 / 16; cgp += G::NG) {
-      float v[16];
-      if (D > 0) {
-        tmem_ld16(tmem + lane_addr + cgp * 16, v);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    for (int k = 0; k < G::P_GROUPS; ++k) {
+      const int cgp = grp + G::NG * k;
+      if (cgp < r16 / 16) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4 *>(to + 4 * ((cgp * 4 + q) ^ (rr & 7))) =
+              make_float4(psum[k][4 * q], psum[k][4 * q + 1], psum[k][4 * q + 2], psum[k][4 * q + 3]);
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4 *>(to + 4 * ((cgp * 4 + q) ^ (rr & 7))) =
-            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
     }
     __syncwarp();
     if (lane < CS) mbar_arrive_cta(B.recv, lane);
@@ -384,7 +422,7 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
 #pragma unroll
     for (int hc = 0; hc < 2; ++hc) {
       uint32_t d[32];
-      tmem_ld32(tmem + lane_addr + RP + 64 * grp + 32 * hc, d);
+      tmem_ld32(tmem + lane_addr + G::D_COL + 64 * grp + 32 * hc, d);
       if (hc == 1) {
         tc_fence_before();
         __syncwarp();
@@ -461,7 +499,10 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
       mbar_init(B.free_mma + 8u * i, 1);
       mbar_init(B.free_out + 8u * i, 4);
     }
-    mbar_init(B.p_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.p_full + 8u * i, 1);
+      mbar_init(B.p_empty + 8u * i, G::WORKERS);
+    }
     for (int i = 0; i < G::NG; ++i) {
       mbar_init(B.d_full + 8u * i, 1);
       mbar_init(B.d_empty + 8u * i, 4);
@@ -569,24 +610,24 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
         const uint32_t id = tc_idesc<XT>(r16, false, UP == 1);
         const uint64_t wd0 = tc_desc(sbase + G::X_BYTES, UP == 0 ? 16 : 8192);
         constexpr uint64_t KW = UP == 0 ? 2 : 128;  // a k-step of W1 in a descriptor's units of 16 bytes
-        bool more = false;
         for (int s = 0; s < D; ++s) {
-          ok = mbar_wait(ready + 8u * slot, use);
+          const int run = s / kTcRun, buf = run & 1;
+          const bool first = s % kTcRun == 0, last = s % kTcRun == kTcRun - 1 || s == D - 1;
+          // the buffer's last run has left it
+          ok = mbar_wait(ready + 8u * slot, use) &&
+               (!first || run < 2 || mbar_wait(B.p_empty + 8u * buf, ((run >> 1) & 1) ^ 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t at = (uint64_t)(slot * (G::SLOT >> 4));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            tc_mma(tmem, xd0 + at + 2 * k, wd0 + at + KW * k, id, more);
-            more = true;
-          }
+          for (int k = 0; k < 4; ++k) tc_mma(tmem + buf * RP, xd0 + at + 2 * k, wd0 + at + KW * k, id, k > 0 || !first);
           umma_commit(B.free_mma + 8u * slot);
+          if (last) umma_commit(B.p_full + 8u * buf);
           if (++slot == NS) {
             slot = 0;
             use ^= 1;
           }
         }
-        if (ok && D > 0) umma_commit(B.p_full);
       }
       // up: 64 output columns a step, A operand t (hi, then lo); W2 = B [64 c][r]
       // (K-major) forward, A [r][64 c] (MN-major) in the gradient
@@ -605,7 +646,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 #pragma unroll
           for (int k = 0; k < RP / 16; ++k)
             if (k < ks)
-              tc_mma(tmem + RP + 64 * buf, td + (part * G::BLOCKS + k / 4) * (kTcRows * 128 >> 4) + 2 * (k % 4),
+              tc_mma(tmem + G::D_COL + 64 * buf, td + (part * G::BLOCKS + k / 4) * (kTcRows * 128 >> 4) + 2 * (k % 4),
                      UP == 0 ? wd + (k / 4) * 512 + 2 * (k % 4) : wd + 128 * k, id, part > 0 || k > 0);
         umma_commit(B.d_full + 8u * buf);
         if (++slot == NS) {

@@ -1,0 +1,54 @@
+"""How exact the fp32 results of the adapters are over long contractions: t, dt, dA and dB against 64 bits, in the norm.
+
+The element-wise bounds of adapter_ref grow with the length of a sum; these do not hide a sum that is kept in a tensor
+core's accumulator for too long.  Such an accumulator loses up to one step of 2^-23 of the running sum at each
+instruction (it cuts, so the losses do not cancel).  The kernels let at most 16 instructions of 16 products add up
+there before fp32 additions that round to nearest take over.  For terms of random signs the running sum's norm grows
+with the square root of the terms, so 16 instructions lose at most 16 * 2/3 * 2^-23 of it, and n rounded additions, whose
+errors are independent, sqrt(n) * 2^-24; n is 64 for 16384 terms."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from quantized_gemm_group_b200 import bq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+LONG = 16 * 2 / 3 * 2.0 ** -23 + 8 * 2.0 ** -24     # 1.75e-6
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def inputs(M, K, N, R, L, adapter, dtype, lens, seed=3):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    rnd = lambda *s, std=1.0: (torch.randn(s, generator=g, device=DEV) * std).to(dtype)  # noqa: E731
+    x, dy, A, B = rnd(M, K), rnd(M, N, std=0.02), rnd(L, R, K, std=K ** -0.5), rnd(L, N, R, std=0.05)
+    offs = [0]
+    for n in lens:
+        offs.append(offs[-1] + n)
+    assert offs[-1] == M
+    i32 = dict(dtype=torch.int32, device=DEV)
+    tail = (torch.full((L,), R, **i32), torch.full((L,), 0.5, device=DEV), torch.tensor(offs, **i32),
+            torch.full((len(lens),), adapter, **i32))
+    return x, dy, A, B, tail
+
+
+# rows and rank choose the kernel's clusters: two CTAs and one CTA each with one CTA an SM, one CTA with two an SM
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("M,R", [(9000, 64), (19000, 64), (9600, 128)])
+def test_long_segments_down(M, R, dt):
+    C = 14336
+    x, dy, A, B, tail = inputs(M, C, 64, R, 2, 1, DT[dt], [M])
+    t = torch.empty((M, R), device=DEV)
+    bq.bq_lora(x, A, B, *tail, t=t)
+    assert off(t, x.double() @ A[1].double().t()) <= LONG
+    del x
+    x, dy, A, B, tail = inputs(M, 64, C, R, 2, 1, DT[dt], [M])
+    ws = torch.empty((M, R), device=DEV)
+    bq.bq_lora_grad(dy, None, None, A, B, *tail, workspace=ws, need_weights=False)
+    assert off(ws, 0.5 * (dy.double() @ B[1].double())) <= LONG
