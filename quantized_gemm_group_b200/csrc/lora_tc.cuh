@@ -139,6 +139,14 @@ BQ_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Zeros in 16 consecutive columns of this thread's TMEM lane.
+BQ_DEV void tmem_zero16(uint32_t taddr) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(taddr),
+               "r"(0)
+               : "memory");
+}
+BQ_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Two floats as the hi and lo parts of type XT (fp16: scaled by the caller).
 template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t &lo) {
   if (XT == 1) {
@@ -696,6 +704,11 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 // instruction multiplies all of them: bf16 three parts (24 bits); fp16 two,
 // P scaled by a power of two that brings the largest of the CTA's rows into
 // [2^14, 2^15).  X is read once; P once for each CT columns (from L2).
+// The products of the first part leave tensor memory every kWgRun steps and are
+// added in registers (as in lora_tc_kernel: in one run, 8192 rows lost 9e-6 of the
+// gradient's norm).  So that the instructions go on meanwhile it has two places,
+// before and behind the lower parts, which are 2^8 times smaller and stay:
+// even runs multiply [first | lower], odd ones [lower | first] one place further.
 
 struct WgradSide {
   const float *P;     // [M, R]
@@ -715,6 +728,7 @@ struct WgradArgs {
 };
 
 constexpr int kWgRows = 64;      // rows per step
+constexpr int kWgRun = 4;        // steps of a run: 16 instructions
 constexpr int kWgGroups = 4;     // worker warps per TMEM lane quadrant
 constexpr int kWgWorkers = 4 * kWgGroups;
 constexpr int kWgThreads = 32 * (2 + kWgWorkers);
@@ -729,14 +743,19 @@ template <int RP> struct WgradGeom {
   static constexpr int RING = XS * X_BYTES + PS * P_BYTES;
   static constexpr int RECV = CT * RP * 4;
   static_assert(RECV <= RING, "the sums' buffer lies over the ring");
-  static constexpr int bar_off = RING;
+  static constexpr int PPT = kWgRows * RP / 4 / (32 * kWgWorkers);  // quads of P per worker and step
+  static constexpr int wait_off = RING;                  // two steps' quads on their way, each worker its own
+  static constexpr int WAIT_STAGE = PPT * 32 * kWgWorkers * 16;
+  static constexpr int bar_off = RING + 2 * WAIT_STAGE;
   static constexpr int nbar = 2 * XS + 2 * PS + 2;
   static constexpr int max_off = bar_off + 8 * nbar;     // largest |P| (fp16), as bits
   static constexpr int tmem_off = max_off + 4;
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
-  static constexpr int TM_COLS = 512;                    // MB x 3 RP columns in use
-  static constexpr int PPT = kWgRows * RP / 4 / (32 * kWgWorkers);  // quads of P per worker
+  static constexpr int TM_COLS = 512;                    // MB x (first, 2 lower, first) x RP columns
+  static constexpr int D_COLS = 4 * RP;
+  static_assert(MB * D_COLS <= TM_COLS, "tensor memory");
+  static constexpr int SUMS = MB * RP / 16 / kWgGroups;  // groups of 16 ranks whose sums a worker warp keeps
 };
 
 // The 64-row tiles of one adapter, in order: every warp walks all of them and
@@ -800,8 +819,10 @@ struct WgradBars {
   }
 };
 
-// P's quad v as parts at (row m, rank r) of a stage.
-template <int XT> BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r16, float4 v) {
+// P's quad v as parts at (row m, rank r) of a stage; the first part's ranks from
+// column first_at on, the others' from low_at.
+template <int XT>
+BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r16, int first_at, int low_at, float4 v) {
   uint2 part[3];
   if (XT == 1) {
     float f[4] = {v.x, v.y, v.z, v.w};
@@ -823,7 +844,7 @@ template <int XT> BQ_DEV void wgrad_store_p(uint32_t stage, int m, int r, int r1
   }
 #pragma unroll
   for (int p = 0; p < (XT == 1 ? 3 : 2); ++p) {
-    const int n = p * r16 + r;
+    const int n = r + (p == 0 ? first_at : low_at + (p - 1) * r16);
     const uint32_t at = stage + (n >> 6) * (kWgRows * 128) + m * 128 + ((((n & 63) >> 3) ^ (m & 7)) << 4) + (n & 7) * 2;
     asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(part[p].x), "r"(part[p].y) : "memory");
   }
@@ -885,6 +906,15 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
   WgradRows w = {};
   int steps = 0;  // tiles taken
   float2 pscale = make_float2(1.0f, 1.0f);
+  // worker warps: which 128 columns and ranks 16 (cg0 + CG k) onwards a warp's sums are of
+  constexpr int CG = kWgGroups / MB;
+  const int quad = warp & 3, grp = (warp - 2) >> 2, mb = MB == 2 ? grp & 1 : 0, cg0 = grp / MB;
+  const uint32_t lane_tmem = tmem + ((uint32_t)(quad * 32) << 16) + mb * G::D_COLS;
+  float psum[G::SUMS][16];
+#pragma unroll
+  for (int k = 0; k < G::SUMS; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) psum[k][i] = 0.0f;
   if (r_a == 0) {
     // no rank: nothing to sum
   } else if (warp == 0) {
@@ -925,15 +955,18 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         tc_fence_after();
         const uint64_t xd = xd0 + (uint64_t)(slot * (G::X_BYTES >> 4)), pd = pd0 + (uint64_t)(ps * (G::P_BYTES >> 4));
         const int ks = (w.rows + 15) / 16;
+        // the run's place holds zeros: every worker has added its last run and
+        // cleared it before it stored P of a step that came before this one
+        const uint32_t d = tmem + ((steps / kWgRun) & 1) * r16;
 #pragma unroll
         for (int k = 0; k < kWgRows / 16; ++k) {
           if (k >= ks) break;
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
             if (2 * mb >= cblocks) break;
-            tc_mma(tmem + mb * 192, xd + 2 * mb * (kWgRows * 128 >> 4) + 128 * k, pd + 128 * k, id0, steps > 0 || k > 0);
+            tc_mma(d + mb * G::D_COLS, xd + 2 * mb * (kWgRows * 128 >> 4) + 128 * k, pd + 128 * k, id0, steps > 0 || k > 0);
             if (MB == 1 && n1 > 0)
-              tc_mma(tmem + n0, xd + 128 * k, pd + 3 * (kWgRows * 128 >> 4) + 128 * k, id1, steps > 0 || k > 0);
+              tc_mma(d + n0, xd + 128 * k, pd + 3 * (kWgRows * 128 >> 4) + 128 * k, id1, steps > 0 || k > 0);
           }
         }
         umma_commit(B.freed + 8u * slot);
@@ -954,32 +987,32 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     const int wt = (int)threadIdx.x - 64;
     const DropState dst = drop_state(a.drop);
     bool ok = true;
-    if (!is_b) pdl_wait();  // dt is complete; all else was before the kernel that makes it began
-    auto load_p = [&](float4 (&pv)[G::PPT], int row0, int rows) {
+    auto first_col = [&](int place) { return lane_tmem + place * PARTS * r16; };
+    // the first run's instructions start with zeros by themselves, the second's place is cleared here
 #pragma unroll
-      for (int k = 0; k < G::PPT; ++k) {
-        const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
-        pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (m < rows && r < r_a) {
-          pv[k] = __ldcg(reinterpret_cast<const float4 *>(side.P + (int64_t)(row0 + m) * a.R + r));
-          if (r + 1 >= r_a) pv[k].y = 0.0f;
-          if (r + 2 >= r_a) pv[k].z = 0.0f;
-          if (r + 3 >= r_a) pv[k].w = 0.0f;
-        }
-      }
-    };
+    for (int k = 0; k < G::SUMS; ++k)
+      if (cg0 + CG * k < r16 / 16) tmem_zero16(first_col(1) + (cg0 + CG * k) * 16);
+    tmem_wait_st();
+    tc_fence_before();
+    if (!is_b) pdl_wait();  // dt is complete; all else was before the kernel that makes it began
     if (XT == 0) {  // the power of two that brings the largest |P| of these rows below fp16's range
       WgradRows v = {};
       float mx = 0.0f;
       while (wgrad_next(v, a, adapter, rank)) {
         float4 pv[G::PPT];
-        load_p(pv, v.row0, v.rows);
 #pragma unroll
         for (int k = 0; k < G::PPT; ++k) {
+          const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
+          pv[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (m < v.rows && r < r_a) pv[k] = __ldcg(reinterpret_cast<const float4 *>(side.P + (int64_t)(v.row0 + m) * a.R + r));
+        }
+#pragma unroll
+        for (int k = 0; k < G::PPT; ++k) {
+          const int r = 4 * ((wt + k * 32 * kWgWorkers) % (RP / 4));
           const float q[4] = {fabsf(pv[k].x), fabsf(pv[k].y), fabsf(pv[k].z), fabsf(pv[k].w)};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (q[i] <= 3.402823466e38f) mx = fmaxf(mx, q[i]);  // infinite and NaN stay what they are
+            if (q[i] <= 3.402823466e38f && r + i < r_a) mx = fmaxf(mx, q[i]);  // infinite and NaN stay what they are
         }
       }
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
@@ -987,30 +1020,67 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWgWorkers) : "memory");
       pscale = tc_scale(__uint_as_float(*reinterpret_cast<volatile uint32_t *>(smem + G::max_off)));
     }
-    // P is read two steps ahead (one step is shorter than the way to L2 and back)
-    float4 pv[2][G::PPT];
+    // P is read two steps ahead (one step is shorter than the way to L2 and back),
+    // through shared memory that only this worker uses (in registers beside the sums:
+    // dt and both gradients of 8192 rows of 4 adapters, rank 64, 174 us, so 138)
+    const uint32_t mine = sbase + G::wait_off + wt * 16;
     int row0[2], rows[2];
     auto fetch = [&](int b) {
       rows[b] = 0;
       if (wgrad_next(w, a, adapter, rank)) {
         row0[b] = w.row0;
         rows[b] = w.rows;
-        load_p(pv[b], w.row0, w.rows);
+#pragma unroll
+        for (int k = 0; k < G::PPT; ++k) {
+          const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
+          if (m < w.rows && r < r_a)
+            cp_async16(mine + b * G::WAIT_STAGE + k * (32 * kWgWorkers * 16), side.P + (int64_t)(w.row0 + m) * a.R + r);
+        }
       }
+      cp_async_commit();
+    };
+    int run = 0;  // runs added to psum
+    auto add_run = [&](bool clear) {
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < G::SUMS; ++k) {
+        const int cgp = cg0 + CG * k;
+        if (cgp < r16 / 16) {
+          float v[16];
+          tmem_ld16(first_col(run & 1) + cgp * 16, v);
+          if (clear) tmem_zero16(first_col(run & 1) + cgp * 16);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) psum[k][i] += v[i];
+        }
+      }
+      if (clear) tmem_wait_st();
+      tc_fence_before();
+      ++run;
     };
     auto step = [&](int b) {
       const int slot = steps % XS, first = row0[b], n = rows[b];
+      const bool odd = (steps / kWgRun) & 1;
       const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + b * G::P_BYTES;
       if (steps >= PS) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.p_free + 8u * b, ((steps / PS) & 1) ^ 1)) != 0;
       if (!ok) return;
+      cp_async_wait<1>();
 #pragma unroll
       for (int k = 0; k < G::PPT; ++k) {
         const int i = wt + k * 32 * kWgWorkers, m = i / (RP / 4), r = 4 * (i % (RP / 4));
-        float4 v = pv[b][k];
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (m < n && r < r_a) {
+          const uint4 q = lds_v4(mine + b * G::WAIT_STAGE + k * (32 * kWgWorkers * 16));
+          v.x = __uint_as_float(q.x);  // what lies behind the rank may be anything
+          if (r + 1 < r_a) v.y = __uint_as_float(q.y);
+          if (r + 2 < r_a) v.z = __uint_as_float(q.z);
+          if (r + 3 < r_a) v.w = __uint_as_float(q.w);
+        }
         if (XT == 0) v = make_float4(v.x * pscale.y, v.y * pscale.y, v.z * pscale.y, v.w * pscale.y);
-        if (r < r16) wgrad_store_p<XT>(pb, m, r, r16, v);
+        if (r < r16) wgrad_store_p<XT>(pb, m, r, r16, odd ? (PARTS - 1) * r16 : 0, odd ? 0 : r16, v);
       }
       fetch(b);
+      // the wait above was for the last step of the run before this one
+      if (b == 1 && steps % kWgRun == 1 && steps > kWgRun) add_run(true);
       if (masked || (n & 15)) {
         constexpr int PT = 2 * MB * kWgRows * 8 / (32 * kWgWorkers);  // 16-byte chunks per worker
         ok = __all_sync(0xffffffffu, mbar_wait(B.full + 8u * slot, (steps / XS) & 1)) != 0;
@@ -1033,7 +1103,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       if (lane == 0) mbar_arrive(B.ready + 8u * b);
       ++steps;
     };
-    static_assert(PS == 2, "a register buffer for each stage of P");
+    static_assert(PS == 2, "a buffer for each stage of P; step s waits for step s - 2");
     fetch(0);
     fetch(1);
     while (ok && rows[0] > 0) {
@@ -1042,6 +1112,8 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       step(1);
     }
     if (ok) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.d_full, 0)) != 0;
+    if (ok)
+      while (run < (steps + kWgRun - 1) / kWgRun) add_run(false);
     if (!ok && lane == 0) {
       if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
       *abort = 1;
@@ -1066,20 +1138,24 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
   const int per_r = r16 / CS, own = CT / CS;  // ranks of dA / columns of dB that one CTA owns
   if (warp >= 2 && r_a > 0) {
     // the warps of a quadrant share its blocks of 128 columns and the ranks
-    const int quad = warp & 3, grp = (warp - 2) >> 2, mb = MB == 2 ? grp & 1 : 0, c = mb * 128 + quad * 32 + lane;
-    const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + mb * 192;
-    for (int cgp = grp / MB; cgp < r16 / 16; cgp += kWgGroups / MB) {
+    const int c = mb * 128 + quad * 32 + lane;
+#pragma unroll
+    for (int k = 0; k < G::SUMS; ++k) {
+      const int cgp = cg0 + CG * k;
+      if (cgp >= r16 / 16) break;
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0.0f;
       if (steps > 0) {
 #pragma unroll
-        for (int p = PARTS - 1; p >= 0; --p) {  // the smallest part first
+        for (int p = PARTS - 1; p > 0; --p) {  // the smallest part first
           float q[16];
-          tmem_ld16(at + p * r16 + cgp * 16, q);
+          tmem_ld16(lane_tmem + p * r16 + cgp * 16, q);
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] += q[i];
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += psum[k][i];
       }
       if (XT == 0) {
 #pragma unroll

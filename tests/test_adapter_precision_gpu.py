@@ -52,3 +52,18 @@ def test_long_segments_down(M, R, dt):
     ws = torch.empty((M, R), device=DEV)
     bq.bq_lora_grad(dy, None, None, A, B, *tail, workspace=ws, need_weights=False)
     assert off(ws, 0.5 * (dy.double() @ B[1].double())) <= LONG
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("K,N,R", [(4096, 16384, 64), (2048, 8192, 128)])
+@pytest.mark.parametrize("lens", [[8229], [5000, 3001]])
+def test_weight_gradients(K, N, R, lens, dt):
+    """So many columns that one CTA takes all rows of a tile; dA against the dt that the call left in its workspace."""
+    M = sum(lens)
+    x, dy, A, B, tail = inputs(M, K, N, R, 2, 1, DT[dt], lens)
+    t = x.float() @ A[1].float().t()
+    ws = torch.empty((M, R), device=DEV)
+    _, dA, dB = bq.bq_lora_grad(dy, x, t, A, B, *tail, workspace=ws, need_dx=False)
+    assert off(dA[1], ws.double().t() @ x.double()) <= LONG
+    assert off(dB[1], 0.5 * (dy.double().t() @ t.double())) <= LONG
+    assert bool((dA[0] == 0).all()) and bool((dB[0] == 0).all())
