@@ -1063,6 +1063,8 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       const uint32_t xb = sbase + slot * G::X_BYTES, pb = sbase + XS * G::X_BYTES + b * G::P_BYTES;
       if (steps >= PS) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.p_free + 8u * b, ((steps / PS) & 1) ^ 1)) != 0;
       if (!ok) return;
+      // the wait above was for the last step of the run before this one
+      if (b == 1 && steps % kWgRun == 1 && steps > kWgRun) add_run(true);
       cp_async_wait<1>();
 #pragma unroll
       for (int k = 0; k < G::PPT; ++k) {
@@ -1079,8 +1081,6 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
         if (r < r16) wgrad_store_p<XT>(pb, m, r, r16, odd ? (PARTS - 1) * r16 : 0, odd ? 0 : r16, v);
       }
       fetch(b);
-      // the wait above was for the last step of the run before this one
-      if (b == 1 && steps % kWgRun == 1 && steps > kWgRun) add_run(true);
       if (masked || (n & 15)) {
         constexpr int PT = 2 * MB * kWgRows * 8 / (32 * kWgWorkers);  // 16-byte chunks per worker
         ok = __all_sync(0xffffffffu, mbar_wait(B.full + 8u * slot, (steps / XS) & 1)) != 0;
