@@ -6,6 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/bq.h"
 #include "common.cuh"
@@ -955,9 +956,12 @@ bq_status launch_lora_t(LoraArgs a, cudaStream_t st) {
   a.CS = cs;
   a.slice_c = (int)round_up((a.Ci + cs - 1) / cs, G::SC);
   a.slice_o = (int)round_up((a.Co + cs - 1) / cs, 32);
-  constexpr auto kern = lora_kernel<XT, UP, RP>;
-  if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
-  return launch_cluster(kern, tiles * cs, cs, kLoraThreads, G::TOTAL, overlap_mode() >= 1, st, a);
+  const auto launch = [&](auto apart) {
+    constexpr auto kern = lora_kernel<XT, UP, RP, decltype(apart)::value>;
+    if (!ensure_smem<kern>(G::TOTAL)) return BQ_ERR_CUDA;
+    return launch_cluster(kern, tiles * cs, cs, kLoraThreads, G::TOTAL, overlap_mode() >= 1, st, a);
+  };
+  return a.slice_c > kLoraRun * G::SC ? launch(std::true_type{}) : launch(std::false_type{});
 }
 
 // Clusters of cs CTAs that the GPU holds at once, two CTAs an SM, with what

@@ -55,6 +55,13 @@ namespace cg = cooperative_groups;
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraRows = 16;  // rows per tile
+// Steps down (of two products each) that a CTA lets add up in the tensor core.  Its
+// additions cut where fp32 additions round: 56 steps (14336 columns in one CTA)
+// lost 2e-6 of t's norm, plain fp32 products 1e-6, 16 steps lose 0.6e-6.  CTAs with
+// more (APART) add each step's products to the sums in fp32.  That costs up to 8 %
+// (1536 rows in 64 segments, 14336 -> 4096, rank 16 48 instead of 45 us), so it is a
+// kernel of its own.
+constexpr int kLoraRun = 16;
 
 struct LoraArgs {
   const uint16_t *x;      // [M, Ci] rows of stride ldx: x, or dy
@@ -279,7 +286,7 @@ template <int UP, int RP, int SC> BQ_DEV uint32_t down_offset(int r, int c) {
 }
 
 // grid = CS x tiles, cluster = (CS, 1, 1).
-template <int XT, int UP, int RP>
+template <int XT, int UP, int RP, bool APART>
 __global__ void __launch_bounds__(kLoraThreads, (RP == 128 || (XT == 0 && RP == 64)) ? 1 : 2)
 lora_kernel(LoraArgs a) {
   using G = LoraGeom<UP, RP>;
@@ -356,6 +363,10 @@ lora_kernel(LoraArgs a) {
   };
 
   float acc[NT][4];
+  auto add4 = [](float (&s)[4], const float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] += v[i];
+  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -383,7 +394,28 @@ lora_kernel(LoraArgs a) {
     }
     const uint32_t stage = sbase + (step % NST) * G::STAGE;
     const uint32_t fa[2][4] = {{cur[0].x, cur[1].x, cur[0].y, cur[1].y}, {cur[0].z, cur[1].z, cur[0].w, cur[1].w}};
-    if (UP == 0) {
+    if (UP == 0 && APART) {
+      // four tiles at a time, so that their products do not wait for one another
+      constexpr int TW = NT < 4 ? NT : 4;
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += TW)
+        if (n0 < nt_used) {
+          uint4 w[TW];
+          float v[TW][4];
+#pragma unroll
+          for (int j = 0; j < TW; ++j) {
+            w[j] = lds_v4(stage + down_offset<UP, RP, SC>((n0 + j) * 8 + g, 4 * warp + t4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] = 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < TW; ++j) MmaT<XT>::mma(v[j], fa[0], w[j].x, w[j].y);
+#pragma unroll
+          for (int j = 0; j < TW; ++j) MmaT<XT>::mma(v[j], fa[1], w[j].z, w[j].w);
+#pragma unroll
+          for (int j = 0; j < TW; ++j) add4(acc[n0 + j], v[j]);
+        }
+    } else if (UP == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         if (nt < nt_used) {
@@ -398,12 +430,17 @@ lora_kernel(LoraArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; nt += 2)
         if (nt < nt_used) {
+          float v[2][4] = {};
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
             uint32_t w[4];
             ldmatrix_x4_trans(w, stage + down_offset<UP, RP, SC>(row + 4 * ks, nt + nx));
-            MmaT<XT>::mma(acc[nt], fa[ks], w[0], w[1]);
-            MmaT<XT>::mma(acc[nt + 1], fa[ks], w[2], w[3]);
+            MmaT<XT>::mma(APART ? v[0] : acc[nt], fa[ks], w[0], w[1]);
+            MmaT<XT>::mma(APART ? v[1] : acc[nt + 1], fa[ks], w[2], w[3]);
+          }
+          if (APART) {
+            add4(acc[nt], v[0]);
+            add4(acc[nt + 1], v[1]);
           }
         }
     }

@@ -5,7 +5,8 @@ core's accumulator for too long.  Such an accumulator loses up to one step of 2^
 instruction (it cuts, so the losses do not cancel).  The kernels let at most 16 instructions of 16 products add up
 there before fp32 additions that round to nearest take over.  For terms of random signs the running sum's norm grows
 with the square root of the terms, so 16 instructions lose at most 16 * 2/3 * 2^-23 of it, and n rounded additions, whose
-errors are independent, sqrt(n) * 2^-24; n is 64 for 16384 terms."""
+errors are independent, sqrt(n) * 2^-24; n is 64 for 16384 terms.  The kernel of short segments adds
+the sums of two instructions, each possibly cutting twice, where a warp has more than 32 of them, up to 64 such sums."""
 from __future__ import annotations
 
 import pytest
@@ -17,6 +18,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
 LONG = 16 * 2 / 3 * 2.0 ** -23 + 8 * 2.0 ** -24     # 1.75e-6
+SHORT = 4 * 2 / 3 * 2.0 ** -23 + 8 * 2.0 ** -24     # 0.80e-6
 
 
 def off(got, want):
@@ -52,6 +54,22 @@ def test_long_segments_down(M, R, dt):
     ws = torch.empty((M, R), device=DEV)
     bq.bq_lora_grad(dy, None, None, A, B, *tail, workspace=ws, need_weights=False)
     assert off(ws, 0.5 * (dy.double() @ B[1].double())) <= LONG
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("R", [16, 64, 128])
+def test_short_segments_down(R, dt):
+    """Enough segments that one CTA takes a tile's whole contraction."""
+    C, lens = 14336, [20] * 160
+    M = sum(lens)
+    x, dy, A, B, tail = inputs(M, C, 64, R, 2, 1, DT[dt], lens)
+    t = torch.empty((M, R), device=DEV)
+    bq.bq_lora(x, A, B, *tail, t=t)
+    assert off(t, x.double() @ A[1].double().t()) <= SHORT
+    x, dy, A, B, tail = inputs(M, 64, C, R, 2, 1, DT[dt], lens)
+    ws = torch.empty((M, R), device=DEV)
+    bq.bq_lora_grad(dy, None, None, A, B, *tail, workspace=ws, need_weights=False)
+    assert off(ws, 0.5 * (dy.double() @ B[1].double())) <= SHORT
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
