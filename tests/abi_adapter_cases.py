@@ -102,3 +102,10 @@ def test_grad(L):
 def test_in_place_means_the_same_rows(L):
     assert forward(L, ldbase=80) == bq.BQ_ERR_SHAPE
     assert grad(L, ldbase=80) == bq.BQ_ERR_SHAPE
+
+
+def test_a_generator_is_wanted_without_rows_too(L):
+    """dA and dB of an empty batch are still written by a kernel."""
+    for kw in (dict(M=0), dict(S=0)):
+        assert grad(L, rng=0, **kw) == bq.BQ_ERR_NULL
+    assert grad(L, rng=0, M=0, p=0.0, dA=0, dB=0) == bq.BQ_OK
