@@ -85,3 +85,40 @@ def test_weight_gradients(K, N, R, lens, dt):
     assert off(dA[1], ws.double().t() @ x.double()) <= LONG
     assert off(dB[1], 0.5 * (dy.double().t() @ t.double())) <= LONG
     assert bool((dA[0] == 0).all()) and bool((dB[0] == 0).all())
+
+
+# t enters its second product as two 16-bit parts: bf16 keeps 2 x 8 bits and a sign, off by at most 2^-17 of t; fp16 2 x 11
+# bits, 2^-22.  One product each, two cutting additions and the fp32 addition of the base: 3 * 2^-23.
+PARTS = {torch.bfloat16: 2.0 ** -17 + 3 * 2.0 ** -23, torch.float16: 2.0 ** -22 + 3 * 2.0 ** -23}
+STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("R", [8, 64, 128])
+@pytest.mark.parametrize("M", [16, 200])
+def test_second_product(M, R, dt):
+    """Rank 1 and a single element of x (of dy) in each row, so that t (dt) is one exact product; the base is the negative
+    result rounded to 16 bits, so that what is left shows the error of the product itself."""
+    d = DT[dt]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + R)
+    rnd = lambda *s: (torch.rand(s, generator=g, device=DEV) + 1).to(d)  # noqa: E731
+    one = dict(dtype=torch.int32, device=DEV)
+    tail = (torch.ones(1, **one), torch.ones(1, device=DEV), torch.tensor([0, M], **one), torch.zeros(1, **one))
+    N = 256
+    v, first, up = rnd(M), rnd(1), rnd(N)
+    x = torch.zeros((M, 8), dtype=d, device=DEV)
+    x[:, 3] = v
+    A, B = torch.zeros((1, R, 8), dtype=d, device=DEV), torch.zeros((1, N, R), dtype=d, device=DEV)
+    A[0, 0, 3], B[0, :, 0] = first[0], up
+    whole = (v.double() * first.double())[:, None] * up.double()[None]
+    base = (-whole).to(d)
+    want = whole + base.double()
+    bound = whole * PARTS[d] + STEP[d] * want.abs() + 2.0 ** -25
+    y = bq.bq_lora(x, A, B, *tail, base=base)
+    assert bool(((y.double() - want).abs() <= bound).all())
+    # the gradient: dy takes x's place, A and B each other's
+    A, B = torch.zeros((1, R, N), dtype=d, device=DEV), torch.zeros((1, 8, R), dtype=d, device=DEV)
+    B[0, 3, 0], A[0, 0] = first[0], up
+    dx, _, _ = bq.bq_lora_grad(x, None, None, A, B, *tail, base=base, need_weights=False)
+    assert bool(((dx.double() - want).abs() <= bound).all())
