@@ -1143,8 +1143,9 @@ bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
     if (q.dx && q.base == q.dx && M > 1 && q.ldbase != q.lddx) return BQ_ERR_SHAPE;
     if (q.dx && (s = lora_matrix(q.A, L, K, K)) != BQ_OK) return s;
     if (need_dt && (s = lora_matrix(q.B, L, N, N)) != BQ_OK) return s;
-    if (!q.seg_off || !q.seg_adapter || (need_dt && !q.dt) || (q.dB && !q.t) || (a.drop.thr && !q.rng)) return BQ_ERR_NULL;
+    if (!q.seg_off || !q.seg_adapter || (need_dt && !q.dt) || (q.dB && !q.t)) return BQ_ERR_NULL;
   }
+  if (a.drop.thr && !q.rng) return BQ_ERR_NULL;  // without rows, too
   if (L && (!q.ranks || !q.scales)) return BQ_ERR_NULL;
   if (!aligned(q.seg_off, 4) || !aligned(q.seg_adapter, 4) || !aligned(q.ranks, 4) || !aligned(q.scales, 4) ||
       !aligned(q.t, 16) || !aligned(q.dt, 16) || !aligned(q.dA, 16) || !aligned(q.dB, 16) ||
@@ -1189,7 +1190,7 @@ bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
   w.R = R;
   w.L = L;
   w.S = rows ? S : 0;
-  w.drop = a.drop;
+  if (rows) w.drop = a.drop;  // without rows there is nothing to mask, and rng is not read
   const WgradInputs in = {q.x, q.dy, M == 1 ? K : q.ldx, M == 1 ? N : q.lddy};
   // launched over the kernel that makes dt whatever BQ_OPT_LINEAR_OVERLAP says: both are
   // this call's, and dA's part waits for it (dB's does not read dt)

@@ -985,7 +985,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     __syncwarp();
   } else {
     const int wt = (int)threadIdx.x - 64;
-    const DropState dst = drop_state(a.drop);
+    const DropState dst = masked ? drop_state(a.drop) : DropState{};
     bool ok = true;
     auto first_col = [&](int place) { return lane_tmem + place * PARTS * r16; };
     // the first run's instructions start with zeros by themselves, the second's place is cleared here
