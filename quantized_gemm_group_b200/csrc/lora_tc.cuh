@@ -1155,7 +1155,8 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
           for (int i = 0; i < 16; ++i) v[i] += q[i];
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += psum[k][i];
+        for (int i = 0; i < 16; ++i)  // an infinity times a lower part that is 0 or of the other sign would give NaN
+          v[i] = fabsf(psum[k][i]) <= 3.402823466e38f ? v[i] + psum[k][i] : psum[k][i];
       }
       if (XT == 0) {
 #pragma unroll
