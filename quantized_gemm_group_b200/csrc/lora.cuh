@@ -27,10 +27,9 @@
 // contraction may run in any order as long as both operands use the same one,
 // so x needs no shared memory and dropout is applied to the loaded registers,
 // one generator block a load.  The pool goes through a cp.async ring.
-// Up: t (fp32) is split into two bf16 parts t = hi + lo (relative error below
-// 2^-17; one bf16 would lose 2^-9 of it), two mma.sync a step.  fp16
-// pools are split into two bf16 parts as well (11 bits = 8 + 3, exact): t does
-// not have fp16's range.  A warp takes 32 output columns of the tile; the
+// Up: t (fp32) is split into two 16-bit parts t = hi + lo, two mma.sync a step:
+// bf16 within 2^-17 (one bf16 would lose 2^-9 of t), fp16 within 2^-22 of the row's
+// largest, which a power of two brings into fp16's range first.  A warp takes 32 output columns of the tile; the
 // column that fragment slot n of tile j stands for is 8 (n / 2) + 2 j + n % 2,
 // so that a lane ends with 8 consecutive columns: base and y move as 16-byte
 // vectors.
@@ -240,15 +239,33 @@ BQ_DEV void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
   if (!(fabsf(rb) <= 3.402823466e38f)) rb = 0.0f;
   lo = pack_bf16(ra, rb);
 }
-// A 16-bit pair of the pool's type as two bf16x2 parts (bf16: lo unused).
-template <int XT> BQ_DEV void pool_parts(uint32_t w, uint32_t &hi, uint32_t &lo) {
+// Two floats as the hi and lo parts of type XT (fp16: scaled by the caller).
+template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t &lo) {
   if (XT == 1) {
-    hi = w;
-    lo = 0;
+    split_bf16(a, b, hi, lo);
   } else {
-    const float2 f = Elem<0>::pair(w);
-    split_bf16(f.x, f.y, hi, lo);
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    float ra = a - f.x, rb = b - f.y;
+    if (!(fabsf(ra) <= 3.402823466e38f)) ra = 0.0f;
+    if (!(fabsf(rb) <= 3.402823466e38f)) rb = 0.0f;
+    const __half2 l = __floats2half2_rn(ra, rb);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
   }
+}
+// 2^e that brings a largest magnitude m into [2^14, 2^15) when divided by it
+// (1 where m is 0 or not finite), as the pair (2^e, 2^-e).
+BQ_DEV float2 tc_scale(float m) {
+  if (!(m > 0.0f) || !(m <= 3.402823466e38f)) return make_float2(1.0f, 1.0f);
+  int e = (int)(__float_as_uint(m) >> 23) - 127 - 14;
+  e = max(-126, min(e, 126));
+  return make_float2(__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23));
+}
+// |v|, 0 where v is not finite (such values do not set a row's power of two).
+BQ_DEV float finite_abs(float v) {
+  v = fabsf(v);
+  return v <= 3.402823466e38f ? v : 0.0f;
 }
 
 // Tile geometry for the padded rank RP.  Shared memory holds, one after the
@@ -272,7 +289,8 @@ template <int UP, int RP> struct LoraGeom {
   static constexpr int CLEAR = UP == 1 ? 0 : (MAIN - PARTIAL) / lora_max(UP_STAGE, 1);
   static constexpr int EARLY = CLEAR < DU ? CLEAR : DU;  // stages clear of the sums
   static constexpr int RECV = kLoraRows * RP * 4;
-  static constexpr int TOTAL = MAIN + RECV;
+  static constexpr int SCALE = MAIN + RECV;  // fp16: the rows' powers of two
+  static constexpr int TOTAL = SCALE + kLoraRows * 4;
 };
 
 // Shared-memory byte offset of 16-byte chunk c of row r in a stage of the
@@ -287,7 +305,7 @@ template <int UP, int RP, int SC> BQ_DEV uint32_t down_offset(int r, int c) {
 
 // grid = CS x tiles, cluster = (CS, 1, 1).
 template <int XT, int UP, int RP, bool APART>
-__global__ void __launch_bounds__(kLoraThreads, (RP == 128 || (XT == 0 && RP == 64)) ? 1 : 2)
+__global__ void __launch_bounds__(kLoraThreads, RP == 128 ? 1 : 2)
 lora_kernel(LoraArgs a) {
   using G = LoraGeom<UP, RP>;
   constexpr int SC = G::SC, NST = G::NST;
@@ -561,9 +579,11 @@ lora_kernel(LoraArgs a) {
     const float sc = a.scales[tile.adapter];
     const float pre = (UP == 0) ? a.drop.inv_keep : sc;  // to t (or dt) as stored
     const float post = (UP == 0) ? sc : 1.0f;                          // to what the up step multiplies
-    for (int i = 4 * (int)threadIdx.x; i < per; i += 4 * kLoraThreads) {
+    for (int i0 = 0; i0 < per; i0 += 4 * kLoraThreads) {  // all lanes take part in a row's maximum
+      const int i = i0 + 4 * (int)threadIdx.x;
+      const bool own = i < per;
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int q = 0; q < CS; ++q) {
+      for (int q = 0; own && q < CS; ++q) {
         const float4 p = *reinterpret_cast<const float4 *>(recv + q * per + i);
         v[0] += p.x;
         v[1] += p.y;
@@ -573,11 +593,21 @@ lora_kernel(LoraArgs a) {
       const int e = rank * per + i, m = e / RP, r = e % RP;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = (r + k < r_a) ? v[k] * pre : 0.0f;
-      if (a.t && m < tile.rows && r < a.R)
+      if (a.t && own && m < tile.rows && r < a.R)
         *reinterpret_cast<float4 *>(a.t + (int64_t)(tile.row0 + m) * a.R + r) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] *= post;
+      float2 rs = make_float2(1.0f, 1.0f);
+      if (XT == 0) {
+        float mx = fmaxf(fmaxf(finite_abs(v[0]), finite_abs(v[1])), fmaxf(finite_abs(v[2]), finite_abs(v[3])));
+#pragma unroll
+        for (int o = 1; o < RP / 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        rs = tc_scale(mx);
+      }
+      if (!own) continue;
       uint2 hi, lo;
-      split_bf16(v[0] * post, v[1] * post, hi.x, lo.x);
-      split_bf16(v[2] * post, v[3] * post, hi.y, lo.y);
+      tc_split<XT>(v[0] * rs.y, v[1] * rs.y, hi.x, lo.x);
+      tc_split<XT>(v[2] * rs.y, v[3] * rs.y, hi.y, lo.y);
       int c = r >> 3;
       if (RP >= 64) c ^= (m & 1) << 2;
       const int at = m * RP * 2 + c * 16 + (r & 7) * 2;
@@ -585,6 +615,7 @@ lora_kernel(LoraArgs a) {
         uint8_t *tt = cluster.map_shared_rank(smem, q);
         *reinterpret_cast<uint2 *>(tt + at) = hi;
         *reinterpret_cast<uint2 *>(tt + kLoraRows * RP * 2 + at) = lo;
+        if (XT == 0 && r == 0) *reinterpret_cast<float *>(tt + G::SCALE + 4 * m) = rs.x;
       }
     }
   }
@@ -592,6 +623,11 @@ lora_kernel(LoraArgs a) {
 
   const uint32_t tbase = sbase, wbase = sbase + G::T_BYTES + warp * G::WT_BYTES;
   const float out_scale = (UP == 1) ? a.drop.inv_keep : 1.0f;
+  float row_scale[2] = {1.0f, 1.0f};
+  if (XT == 0) {
+    row_scale[0] = *reinterpret_cast<const float *>(smem + G::SCALE + 4 * g);
+    row_scale[1] = *reinterpret_cast<const float *>(smem + G::SCALE + 4 * (g + 8));
+  }
   int turn = 0;
   for (int cb = o_begin + 32 * warp; cb < o_end; cb += 32 * kLoraWarps, ++turn) {
     const uint32_t from = up_stage(turn) + lane * 16;
@@ -706,12 +742,8 @@ lora_kernel(LoraArgs a) {
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t h0, l0, h1, l1;
-          pool_parts<XT>(w[j][i][ks][0], h0, l0);
-          pool_parts<XT>(w[j][i][ks][1], h1, l1);
-          MmaT<1>::mma(d[j], fh[ks], h0, h1);
-          MmaT<1>::mma(d[j], fl[ks], h0, h1);
-          if (XT == 0) MmaT<1>::mma(d[j], fh[ks], l0, l1);
+          MmaT<XT>::mma(d[j], fh[ks], w[j][i][ks][0], w[j][i][ks][1]);
+          MmaT<XT>::mma(d[j], fl[ks], w[j][i][ks][0], w[j][i][ks][1]);
         }
     }
 #pragma unroll
@@ -725,6 +757,10 @@ lora_kernel(LoraArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float v0 = d[j][2 * half], v1 = d[j][2 * half + 1];
+        if (XT == 0) {
+          v0 *= row_scale[half];
+          v1 *= row_scale[half];
+        }
         if (UP == 1 && drop) {
           v0 = drop_keep(keep, 2 * j, dst.thr_hi) ? v0 * out_scale : 0.0f;
           v1 = drop_keep(keep, 2 * j + 1, dst.thr_hi) ? v1 * out_scale : 0.0f;

@@ -147,30 +147,6 @@ BQ_DEV void tmem_zero16(uint32_t taddr) {
 }
 BQ_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two floats as the hi and lo parts of type XT (fp16: scaled by the caller).
-template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t &lo) {
-  if (XT == 1) {
-    split_bf16(a, b, hi, lo);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    float ra = a - f.x, rb = b - f.y;
-    if (!(fabsf(ra) <= 3.402823466e38f)) ra = 0.0f;
-    if (!(fabsf(rb) <= 3.402823466e38f)) rb = 0.0f;
-    const __half2 l = __floats2half2_rn(ra, rb);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-  }
-}
-// 2^e that brings a largest magnitude m into [2^14, 2^15) when divided by it
-// (1 where m is 0 or not finite), as the pair (2^e, 2^-e).
-BQ_DEV float2 tc_scale(float m) {
-  if (!(m > 0.0f) || !(m <= 3.402823466e38f)) return make_float2(1.0f, 1.0f);
-  int e = (int)(__float_as_uint(m) >> 23) - 127 - 14;
-  e = max(-126, min(e, 126));
-  return make_float2(__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23));
-}
-
 // ---------------------------------------------------------------------------
 // forward / input gradient
 // ---------------------------------------------------------------------------
