@@ -28,9 +28,9 @@
 // so x needs no shared memory and dropout is applied to the loaded registers,
 // one generator block a load.  The pool goes through a cp.async ring.
 // Up: t (fp32) is split into two 16-bit parts t = hi + lo, two mma.sync a step:
-// bf16 within 2^-17 (one bf16 would lose 2^-9 of t), fp16 within 2^-22 of the row's
-// largest, which a power of two brings into fp16's range first.  A warp takes 32 output columns of the tile; the
-// column that fragment slot n of tile j stands for is 8 (n / 2) + 2 j + n % 2,
+// bf16 within 2^-16 (one bf16 would lose 2^-9 of t), fp16 within 2^-21 and 2^-38 of the
+// row's largest, which a power of two brings into fp16's range first.  A warp takes
+// 32 output columns of the tile; the column that fragment slot n of tile j stands for is 8 (n / 2) + 2 j + n % 2,
 // so that a lane ends with 8 consecutive columns: base and y move as 16-byte
 // vectors.
 //
@@ -252,6 +252,34 @@ template <int XT> BQ_DEV void tc_split(float a, float b, uint32_t &hi, uint32_t 
     const __half2 l = __floats2half2_rn(ra, rb);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
+  }
+}
+// The parts for a product whose other factor may be infinite: hi is cut, lo = a - hi
+// has its sign and is not 0 unless a is, so that both parts times an infinity give
+// the same one (with hi rounded, lo of the other sign or 0 would make it NaN).  Off
+// by 2^-16 of a (bf16), 2^-21 and 2^-24 (fp16).  Where lo would be 0 it is 2^-24 of hi;
+// fp16 has no less than 2^-24, 2^-38 of the row's largest after tc_scale.  Values that
+// are too small for that (bf16 below 2^-102, fp16 below 2^-24) keep lo = 0.
+BQ_DEV float same_sign_rest(float a, float h, float least) {
+  const float r = a - h;  // exact; NaN where a is not finite
+  return fabsf(r) > 0.0f ? r : h * least;
+}
+template <int XT> BQ_DEV void split_same_sign(float a, float b, uint32_t &hi, uint32_t &lo) {
+  if (XT == 1) {
+    const float ha = isnan(a) ? a : __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+    const float hb = isnan(b) ? b : __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+    hi = pack_bf16(ha, hb);
+    lo = pack_bf16(same_sign_rest(a, ha, 0x1p-24f), same_sign_rest(b, hb, 0x1p-24f));
+  } else {
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    const float2 h = Elem<0>::pair(hi);
+    const __half2 l = __floats2half2_rn(same_sign_rest(a, h.x, 1.0f), same_sign_rest(b, h.y, 1.0f));
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+    // exact values, and rests that round to 0
+    if (h.x != 0.0f && (a == h.x || !(lo & 0x7fffu)) && fabsf(a) <= 3.402823466e38f)
+      lo = (lo & 0xffff0000u) | (hi & 0x8000u) | 1u;
+    if (h.y != 0.0f && (b == h.y || !(lo & 0x7fff0000u)) && fabsf(b) <= 3.402823466e38f)
+      lo = (lo & 0x0000ffffu) | (hi & 0x80000000u) | 0x10000u;
   }
 }
 // 2^e that brings a largest magnitude m into [2^14, 2^15) when divided by it
@@ -606,8 +634,8 @@ lora_kernel(LoraArgs a) {
       }
       if (!own) continue;
       uint2 hi, lo;
-      tc_split<XT>(v[0] * rs.y, v[1] * rs.y, hi.x, lo.x);
-      tc_split<XT>(v[2] * rs.y, v[3] * rs.y, hi.y, lo.y);
+      split_same_sign<XT>(v[0] * rs.y, v[1] * rs.y, hi.x, lo.x);
+      split_same_sign<XT>(v[2] * rs.y, v[3] * rs.y, hi.y, lo.y);
       int c = r >> 3;
       if (RP >= 64) c ^= (m & 1) << 2;
       const int at = m * RP * 2 + c * 16 + (r & 7) * 2;

@@ -22,9 +22,10 @@
 // 43 where it takes 33 (4096 rows, 4096 -> 4096, rank 64): a second launch and
 // the sums' way through L2 cost more than the exchange.
 //
-// Rounding: t enters the up product as two 16-bit parts, t = hi + lo (bf16:
-// relative error below 2^-17; fp16: the row is first scaled by a power of two so
-// that its largest value lies in [2^14, 2^15), error below 2^-22 of it).  One
+// Rounding: t enters the up product as two 16-bit parts, t = hi + lo of one sign
+// (split_same_sign; bf16: relative error below 2^-16; fp16: the row is first scaled by
+// a power of two so that its largest value lies in [2^14, 2^15), error below 2^-21 of
+// the value and 2^-38 of the largest).  One
 // part would lose 2^-9; the second costs a matrix instruction and no traffic.
 // Long sums leave the tensor core's accumulator every 16 instructions (kTcRun).
 //
@@ -343,15 +344,15 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
       if (k * 32 * G::WORKERS >= own * (RP / 4)) break;
       float2 sc = make_float2(1.0f, 1.0f);
       if (XT == 0) {
-        float mx = fmaxf(fmaxf(fabsf(sum[k][0] * post), fabsf(sum[k][1] * post)),
-                         fmaxf(fabsf(sum[k][2] * post), fabsf(sum[k][3] * post)));
+        float mx = fmaxf(fmaxf(finite_abs(sum[k][0] * post), finite_abs(sum[k][1] * post)),
+                         fmaxf(finite_abs(sum[k][2] * post), finite_abs(sum[k][3] * post)));
 #pragma unroll
         for (int o = 1; o < RP / 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         sc = tc_scale(mx);
       }
       uint2 hi, lo;
-      tc_split<XT>(sum[k][0] * post * sc.y, sum[k][1] * post * sc.y, hi.x, lo.x);
-      tc_split<XT>(sum[k][2] * post * sc.y, sum[k][3] * post * sc.y, hi.y, lo.y);
+      split_same_sign<XT>(sum[k][0] * post * sc.y, sum[k][1] * post * sc.y, hi.x, lo.x);
+      split_same_sign<XT>(sum[k][2] * post * sc.y, sum[k][3] * post * sc.y, hi.y, lo.y);
       const int at = (r >> 6) * (kTcRows * 128) + row * 128 + ((((r & 63) >> 3) ^ (row & 7)) << 4) + (r & 7) * 2;
       if (ml < own && row < kTcRows && r < r16)
         for (int q = 0; q < CS; ++q) {

@@ -33,6 +33,13 @@ def segments(c):
             zip(c.seg_off.tolist(), c.seg_off.tolist()[1:], c.seg_adapter.tolist())]
 
 
+def formula_y(c):
+    y = c.base.double().clone()
+    for a, m, r in segments(c):
+        y[m] += float(c.scales[a]) * (c.x[m].double() @ c.A[a, :r].double().t()) @ c.B[a, :, :r].double().t()
+    return y
+
+
 def formula_grad(c, t):
     dx, dA, dB = c.dbase.double().clone(), torch.zeros_like(c.A.double()), torch.zeros_like(c.B.double())
     for a, m, r in segments(c):
@@ -70,3 +77,30 @@ def test_weight_gradients(lens, R, dt):
     t[1, 2], t[0, 0] = INF, -INF
     _, _, gB = c.grad(t)
     same_kind("dB", gB, formula_grad(c, t)[2], dB)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("R", RANKS)
+@pytest.mark.parametrize("lens", LENS)
+def test_outputs(lens, R, dt):
+    """B in the forward pass and A in the gradient, one infinity in a column and two of either sign in another; x and dy."""
+    c = case(lens, R, dt)
+    y0 = c.forward()
+    t = torch.zeros((c.M, R), device=DEV)
+    c.forward(t=t)
+    dx0 = c.grad(t, need_weights=False)[0]
+    A, B, x, dy = (v.clone() for v in (c.A, c.B, c.x, c.dy))
+    c.B[0, 5, 3] = c.B[1, 199, 0] = INF
+    c.B[1, 64, 2], c.B[1, 64, 4] = -INF, INF
+    same_kind("y", c.forward(), formula_y(c), y0)
+    c.B.copy_(B)
+    c.A[0, 3, 11] = c.A[1, 0, 263] = -INF
+    c.A[1, 2, 70], c.A[1, 4, 70] = -INF, INF
+    same_kind("dx", c.grad(t, need_weights=False)[0], formula_grad(c, t)[0], dx0)
+    c.A.copy_(A)
+    c.x[1, 7] = INF
+    same_kind("y", c.forward(), formula_y(c), y0)
+    c.x = x
+    c.dy[2, 6] = -INF
+    same_kind("dx", c.grad(t, need_weights=False)[0], formula_grad(c, t)[0], dx0)
+    assert bq.bq_device_status() == bq.BQ_OK

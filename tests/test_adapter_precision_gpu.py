@@ -87,9 +87,11 @@ def test_weight_gradients(K, N, R, lens, dt):
     assert bool((dA[0] == 0).all()) and bool((dB[0] == 0).all())
 
 
-# t enters its second product as two 16-bit parts: bf16 keeps 2 x 8 bits and a sign, off by at most 2^-17 of t; fp16 2 x 11
-# bits, 2^-22.  One product each, two cutting additions and the fp32 addition of the base: 3 * 2^-23.
-PARTS = {torch.bfloat16: 2.0 ** -17 + 3 * 2.0 ** -23, torch.float16: 2.0 ** -22 + 3 * 2.0 ** -23}
+# t enters its second product as two 16-bit parts of one sign.  The first is cut: bf16 keeps 8 bits and leaves less than
+# 2^-7 of t, of which the second part's 8 bits lose half a step, 2^-9: 2^-16.  fp16 with 11 bits each: 2^-10 * 2^-11 (2^-12
+# of a rest in [2^-11, 2^-10), so 2^-21 is safe).  A rest of 0 counts as 2^-24.  One product each, two cutting additions
+# and the fp32 addition of the base: 3 * 2^-23.
+PARTS = {torch.bfloat16: 2.0 ** -16 + 4 * 2.0 ** -23, torch.float16: 2.0 ** -21 + 4 * 2.0 ** -23}
 STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 
 
