@@ -1071,6 +1071,7 @@ bq_status bq_dropout(const void *x, bq_dtype dtype, int64_t rows, int64_t cols, 
   DropArgs d = {};
   if (!drop_args(p, rng, &d)) return BQ_ERR_UNSUPPORTED;
   if (rows > 1 && (ldx < cols || ldo < cols)) return BQ_ERR_SHAPE;
+  if (x == out && rows > 1 && ldx != ldo) return BQ_ERR_SHAPE;  // in place means the same rows
   if (rows == 0 || cols == 0) return BQ_OK;
   if (!x || !out || (d.thr && !rng)) return BQ_ERR_NULL;
   const size_t es = dtype == BQ_F32 ? 4 : 2;

@@ -109,3 +109,8 @@ def test_a_generator_is_wanted_without_rows_too(L):
     for kw in (dict(M=0), dict(S=0)):
         assert grad(L, rng=0, **kw) == bq.BQ_ERR_NULL
     assert grad(L, rng=0, M=0, p=0.0, dA=0, dB=0) == bq.BQ_OK
+
+
+def test_dropout_in_place_means_the_same_rows(L):
+    for kw in (dict(ldo=24), dict(ldx=24), dict(ldx=24, dtype=bq.BQ_F32)):
+        assert dropout(L, **kw) == bq.BQ_ERR_SHAPE, kw
