@@ -1191,6 +1191,7 @@ bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream) {
   w.R = R;
   w.L = L;
   w.S = rows ? S : 0;
+  w.check = rows && !need_dt;  // else the kernel that makes dt has looked at the segments
   if (rows) w.drop = a.drop;  // without rows there is nothing to mask, and rng is not read
   const WgradInputs in = {q.x, q.dy, M == 1 ? K : q.ldx, M == 1 ? N : q.lddy};
   // launched over the kernel that makes dt whatever BQ_OPT_LINEAR_OVERLAP says: both are

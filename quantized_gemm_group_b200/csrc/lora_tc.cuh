@@ -702,6 +702,7 @@ struct WgradArgs {
   int64_t M;
   int R, L, S, CS;  // CS: CTAs per cluster, 1, 2, 4 or 8
   DropArgs drop;  // on dA's X
+  bool check;     // bad segments are recorded here
 };
 
 constexpr int kWgRows = 64;      // rows per step
@@ -875,6 +876,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0 && a.S > 0) prefetch_map(map);
+  if (a.check && blockIdx.x == 0 && warp == 2) lora_check_segments(a.seg_off, a.seg_adapter, a.ranks, a.S, a.L, a.R, a.M);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
