@@ -65,3 +65,27 @@ def test_segments_are_checked():
         adapters.segments([1, 2], [0])
     with pytest.raises(ValueError):
         adapters.segments([1, -2], [0, 1])
+
+
+def test_rows_with_a_stride():
+    """Slices of a fused tensor give what their dense copies give; an output with strides is refused."""
+    ly = layer(4)
+    lens = [40, 3, 100]
+    M = sum(lens)
+    wide = lambda cols, seed: synth.activations(M, cols + 48, seed=seed, device=DEV)[:, 24:24 + cols]  # noqa: E731
+    x, dy = wide(ly.K, 3), wide(ly.N, 4)
+    segs = adapters.segments(lens, [0, 1, 0])
+    assert torch.equal(ly(x, segs), ly(x.contiguous(), segs))
+    y, saved = ly.forward(x, segs)
+    want, kept = ly.forward(x.contiguous(), segs)
+    assert torch.equal(y, want)
+    for a, b in zip(ly.backward(dy, saved), ly.backward(dy.contiguous(), kept)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        ly(x, segs, out=wide(ly.N, 5))
+    with pytest.raises(ValueError):
+        ly(x, segs, out=torch.empty((M + 1, ly.N), dtype=x.dtype, device=DEV))
+    W = synth.normal((ly.N, 2 * ly.K), 0.02, seed=4, dtype="f16", device=DEV)[:, ::2]
+    pool = (ly.A, ly.B, ly.ranks, ly.scales)
+    a, b = adapters.AdaptedLinear(W, 4, *pool), adapters.AdaptedLinear(W.contiguous(), 4, *pool)
+    assert all(torch.equal(p, q) for p, q in zip(a.weights, b.weights))

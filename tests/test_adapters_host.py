@@ -103,3 +103,25 @@ def test_reference_gradients_against_differences():
         up[i], down[i] = args[i] + d, args[i] - d
         q = float((dy * (ref.lora(*up, *tail, **kw)[0] - ref.lora(*down, *tail, **kw)[0])).sum()) / 2
         assert abs(float((got * d).sum()) - q) <= 1e-9 * max(1.0, abs(q))
+
+
+def test_adapted_linear_refuses_other_shapes():
+    """The frozen layer's calls read as many packed bytes as the rows are wide: another width is refused before them."""
+    from quantized_gemm_group_b200 import adapters
+    ly = object.__new__(adapters.AdaptedLinear)
+    ly.N, ly.K, ly.bits, ly.group, ly.weights = 64, 128, 4, 128, (None, None, None)
+    ly.A, ly.B = torch.zeros((1, 8, 128)).half(), torch.zeros((1, 64, 8)).half()
+    ly.ranks, ly.scales = torch.zeros(1, dtype=torch.int32), torch.zeros(1)
+    segs = (torch.tensor([0, 2], dtype=torch.int32), torch.tensor([0], dtype=torch.int32))
+    for x in (torch.zeros((2, 256)).half(), torch.zeros((2, 64)).half(), torch.zeros((2, 128)), torch.zeros((1, 2, 128)).half(),
+              torch.zeros((2, 128)).half()):            # wider, narrower, another type, three dimensions, not on a GPU
+        with pytest.raises(ValueError):
+            ly(x, segs)
+        with pytest.raises(ValueError):
+            ly.forward(x, segs)
+    saved = (torch.zeros((2, 128)).half(), torch.zeros((2, 8)), segs, 0.0, None)
+    for dy in (torch.zeros((2, 128)).half(), torch.zeros((2, 64))):
+        with pytest.raises(ValueError):
+            ly.backward(dy, saved)
+    with pytest.raises(ValueError):
+        adapters.AdaptedLinear(torch.zeros((64, 128)).half(), 4, ly.A, ly.B, ly.ranks, ly.scales)
