@@ -317,8 +317,8 @@ bq_status bq_linear_grad_input(const void *dy, bq_dtype dtype, int64_t M, int64_
  * generator and never stored.  The same call on dy gives the gradient: the
  * mask depends on (seed, offset, row, column) alone.
  *   x, out   [rows, cols] of dtype (BQ_F16, BQ_BF16 or BQ_F32), row strides
- *            ldx, ldo >= cols in elements; out may be x with ldo = ldx
- *            (no other overlap).  Any column count (to 2^34, rows to 2^31) and
+ *            ldx, ldo >= cols in elements; out may be x with ldo = ldx (else
+ *            BQ_ERR_SHAPE; no other overlap).  Any column count (to 2^34, rows to 2^31) and
  *            alignment of whole elements; 16-byte aligned rows are the fast path.
  *   p        probability of dropping an element, 0 <= p < 1, rounded to a
  *            multiple of 2^-16 (1 - 2^-17 and above: BQ_ERR_UNSUPPORTED)
@@ -355,9 +355,9 @@ bq_status bq_dropout(const void *x, bq_dtype dtype, int64_t rows, int64_t cols, 
  * -1 .. L - 1 or a rank outside 0 .. R set BQ_ERR_UNSUPPORTED in the device
  * status word; a segment with such offsets is skipped, one with such an
  * adapter gets no contribution.
- * Shapes: K, N and R are multiples of 8, 8 <= R <= 128 (other R:
- * BQ_ERR_UNSUPPORTED), M <= 2^30, K and N <= 2^28; row strides (in elements)
- * are multiples of 8 and rows 16-byte aligned, so a slice of a fused
+ * Shapes: K, N and R are multiples of 8 (else BQ_ERR_SHAPE), 8 <= R <= 128 (R = 0
+ * or above 128: BQ_ERR_UNSUPPORTED), M <= 2^30, K and N <= 2^28 (else
+ * BQ_ERR_SHAPE); row strides (in elements) are multiples of 8 and rows 16-byte aligned, so a slice of a fused
  * projection can be x, base or y.  With BQ_OPT_LINEAR_OVERLAP >= 1 the kernel
  * takes part in the programmatic dependent launches of bq_linear.
  * The arguments of one call, in host memory (read before the call returns):
@@ -401,9 +401,11 @@ typedef struct {
  * bq_lora: t[m] = drop(x)[m] A_a^T, y[m] = base[m] + s_a t[m] B_a^T.
  * Dropout is what bq_dropout(x, p, rng) would give before its rounding.
  * Rows of segments are written in full (those without an adapter: y = base,
- * t = 0; t is 0 behind the rank).  Products are exact and accumulated in
- * fp32, t enters the second product with a relative error below 2^-16, y is
- * rounded once.  y and t do not overlap x.  Deterministic.
+ * t = 0; t is 0 behind the rank).  Products are exact, sums are fp32 (t within
+ * about 1e-6 of its norm, however long the contraction), t enters the second
+ * product with a relative error below 2^-16 (fp16: 2^-21, and 2^-38 of the row's
+ * largest), y is rounded once.  Infinite elements give the infinities and NaN of
+ * the formula.  y and t do not overlap x.  Deterministic.
  */
 bq_status bq_lora(const bq_lora_args *args, void *stream);
 
@@ -417,7 +419,9 @@ bq_status bq_lora(const bq_lora_args *args, void *stream);
  * written in full; dA and dB are written in full (zero behind the rank and
  * for adapters without rows).  16-byte alignment for t, dt, dA and dB.  Two
  * calls in flight must not share dt.  No output overlaps dy, x or t.  Sums
- * over rows are fp32 in a fixed order (deterministic, no atomics).
+ * are fp32 in a fixed order (deterministic, no atomics); dA and dB are within
+ * about 1e-6 of their norms.  rng is wanted with p > 0 even where there are no
+ * rows.
  */
 bq_status bq_lora_grad(const bq_lora_grad_args *args, void *stream);
 
