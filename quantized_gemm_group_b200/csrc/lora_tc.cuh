@@ -1090,6 +1090,7 @@ lora_wgrad_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant_
       if (!ok || rows[1] <= 0) break;
       step(1);
     }
+    cp_async_wait<0>();  // no copy is on its way when the CTA leaves
     if (ok) ok = __all_sync(0xffffffffu, !*abort && mbar_wait(B.d_full, 0)) != 0;
     if (ok)
       while (run < (steps + kWgRun - 1) / kWgRun) add_run(false);
