@@ -491,21 +491,13 @@ lora_kernel(LoraArgs a) {
         }
     }
   };
-  // One copy of the step and register moves, or two that change the buffers
-  // over: 16 requests 14336 -> 4096, rank 64 16.7 against 18.0 us, but 1536 rows
-  // of rank 16 29.8 against 26.3 and 16 requests of rank 128 27.0 against 23.4.
-  if constexpr (RP == 64) {
-#pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
-      run_step(xv[0], xv[1], step);
-      xv[0][0] = xv[1][0];
-      xv[0][1] = xv[1][1];
-    }
-  } else {
-    for (int step = 0; step < steps; step += 2) {
-      run_step(xv[0], xv[1], step);
-      if (step + 1 < steps) run_step(xv[1], xv[0], step + 1);
-    }
+  // Two copies of the step that change the buffers over, as one copy and register
+  // moves gained nothing on the whole: rank 64, 128 requests 14336 -> 4096 50.0 against
+  // 47.6 us, but 61 requests 1032 -> 1000 6.6 against 6.8; 40 shapes within 5 % either
+  // way, 0.3 % in the mean; rank 16 and 128 slower by up to 15 %.
+  for (int step = 0; step < steps; step += 2) {
+    run_step(xv[0], xv[1], step);
+    if (step + 1 < steps) run_step(xv[1], xv[0], step + 1);
   }
   cp_async_wait<0>();
   __syncthreads();
