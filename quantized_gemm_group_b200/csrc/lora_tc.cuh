@@ -22,10 +22,12 @@
 // 43 where it takes 33 (4096 rows, 4096 -> 4096, rank 64): a second launch and
 // the sums' way through L2 cost more than the exchange.
 //
-// Rounding: t enters the up product as two 16-bit parts, t = hi + lo of one sign
-// (split_same_sign; bf16: relative error below 2^-16; fp16: the row is first scaled by
-// a power of two so that its largest value lies in [2^14, 2^15), error below 2^-21 of
-// the value and 2^-38 of the largest).  One
+// Rounding: t enters the up product as two 16-bit parts, t = hi + lo (bf16:
+// relative error below 2^-17; fp16: the row is first scaled by a power of two so
+// that its largest value lies in [2^14, 2^15), error below 2^-22 of the value and 2^-38
+// of the largest).  Their products have sums of their own, so that those of hi say
+// where an infinite element gives an infinity (lora.cuh's kernel gives lo hi's sign
+// instead, which costs a bit).  One
 // part would lose 2^-9; the second costs a matrix instruction and no traffic.
 // Long sums leave the tensor core's accumulator every 16 instructions (kTcRun).
 //
@@ -127,19 +129,25 @@ BQ_DEV void tc_give_up(volatile int *abort) {  // a wait ran out: the other role
   if (!*abort) bq_flag(BQ_FLAG_TIMEOUT);
   *abort = 1;
 }
-// 32 consecutive fp32 columns of this thread's TMEM lane.
-BQ_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+// 16 consecutive fp32 columns of this thread's TMEM lane from each of two places.
+BQ_DEV void tmem_ld16_two(uint32_t a, uint32_t b, float (&v)[16], float (&w)[16]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[16 * k]), "=r"(r[16 * k + 1]), "=r"(r[16 * k + 2]), "=r"(r[16 * k + 3]), "=r"(r[16 * k + 4]),
+          "=r"(r[16 * k + 5]), "=r"(r[16 * k + 6]), "=r"(r[16 * k + 7]), "=r"(r[16 * k + 8]), "=r"(r[16 * k + 9]),
+          "=r"(r[16 * k + 10]), "=r"(r[16 * k + 11]), "=r"(r[16 * k + 12]), "=r"(r[16 * k + 13]), "=r"(r[16 * k + 14]),
+          "=r"(r[16 * k + 15])
+        : "r"(k == 0 ? a : b));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = __uint_as_float(r[i]);
+    w[i] = __uint_as_float(r[16 + i]);
+  }
 }
-
 // Zeros in 16 consecutive columns of this thread's TMEM lane.
 BQ_DEV void tmem_zero16(uint32_t taddr) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(taddr),
@@ -177,9 +185,10 @@ template <int RP, bool DEEP> struct TcGeom {
   static constexpr int tmem_off = scale_off + 4 * kTcRows;
   static constexpr int abort_off = tmem_off + 4;
   static constexpr int total = abort_off + 4 + 1024;
-  static constexpr int D_COL = 2 * RP;              // output: NG x 64 columns behind the two buffers of P
+  // two buffers of P; when all of P has been read, the output: for each of NG
+  // groups 64 columns of hi's products and 64 of lo's
   static constexpr int TM_COLS = DEEP ? 512 : 256;
-  static_assert(D_COL + 64 * NG <= TM_COLS, "tensor memory");
+  static_assert(2 * RP <= TM_COLS && 128 * NG <= TM_COLS, "tensor memory");
   static constexpr int P_GROUPS = RP / 16 / NG;     // groups of 16 ranks whose sums a worker warp keeps
   static constexpr int PER_THREAD = kTcRows * RP / 4 / (32 * WORKERS);  // quads of sums per worker, CS = 1
 };
@@ -351,8 +360,8 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
         sc = tc_scale(mx);
       }
       uint2 hi, lo;
-      split_same_sign<XT>(sum[k][0] * post * sc.y, sum[k][1] * post * sc.y, hi.x, lo.x);
-      split_same_sign<XT>(sum[k][2] * post * sc.y, sum[k][3] * post * sc.y, hi.y, lo.y);
+      tc_split<XT>(sum[k][0] * post * sc.y, sum[k][1] * post * sc.y, hi.x, lo.x);
+      tc_split<XT>(sum[k][2] * post * sc.y, sum[k][3] * post * sc.y, hi.y, lo.y);
       const int at = (r >> 6) * (kTcRows * 128) + row * 128 + ((((r & 63) >> 3) ^ (row & 7)) << 4) + (r & 7) * 2;
       if (ml < own && row < kTcRows && r < r16)
         for (int q = 0; q < CS; ++q) {
@@ -405,30 +414,47 @@ BQ_DEV void lora_tc_workers(const LoraArgs &a, const LoraTile &tile, int r_a, in
     if (!ok) break;
     tc_fence_after();
 #pragma unroll
-    for (int hc = 0; hc < 2; ++hc) {
-      uint32_t d[32];
-      tmem_ld32(tmem + lane_addr + G::D_COL + 64 * grp + 32 * hc, d);
-      if (hc == 1) {
+    for (int hc = 0; hc < 4; ++hc) {
+      float d[16], lo[16];
+      const uint32_t at_hi = tmem + lane_addr + 128 * grp + 16 * hc;
+      tmem_ld16_two(at_hi, at_hi + 64, d, lo);
+      if (hc == 3) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(B.d_empty + 8u * grp);
       }
+      // lo is often 0 or of hi's other sign: where an infinite element of the pool made
+      // its products NaN, hi's alone say what the formula gives
+      float2 any = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t at = xs + m * 128 + (((4 * hc + q) ^ (m & 7)) << 4);
+      for (int i = 0; i < 16; i += 2) any = __fadd2_rn(any, make_float2(lo[i], lo[i + 1]));
+      if (!(fabsf(any.x + any.y) <= 3.402823466e38f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(fabsf(d[i]) <= 3.402823466e38f)) lo[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float2 v = __fadd2_rn(make_float2(d[i], d[i + 1]), make_float2(lo[i], lo[i + 1]));
+        d[i] = v.x;
+        d[i + 1] = v.y;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t at = xs + m * 128 + (((2 * hc + q) ^ (m & 7)) << 4);
         uint4 b = make_uint4(0, 0, 0, 0);
         if (a.base) b = lds_v4(at);
         if (UP == 1 && drop) {
-          const uint4 keep = drop_block(dst, (uint32_t)((col0 >> 3) + 4 * hc + q), (uint32_t)(tile.row0 + m));
+          const uint4 keep = drop_block(dst, (uint32_t)((col0 >> 3) + 2 * hc + q), (uint32_t)(tile.row0 + m));
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            d[8 * q + i] = drop_keep(keep, i, dst.thr_hi) ? __float_as_uint(__uint_as_float(d[8 * q + i]) * a.drop.inv_keep) : 0u;
+            d[8 * q + i] = drop_keep(keep, i, dst.thr_hi) ? d[8 * q + i] * a.drop.inv_keep : 0.0f;
         }
         const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
         uint32_t ow[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 v = make_float2(__uint_as_float(d[8 * q + 2 * i]), __uint_as_float(d[8 * q + 2 * i + 1]));
+          float2 v = make_float2(d[8 * q + 2 * i], d[8 * q + 2 * i + 1]);
           const float2 bf = Elem<XT>::pair(bw[i]);
           v = XT == 0 ? __ffma2_rn(v, make_float2(row_scale, row_scale), bf) : __fadd2_rn(v, bf);
           ow[i] = pack_pair<XT>(v);
@@ -614,7 +640,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
           }
         }
       }
-      // up: 64 output columns a step, A operand t (hi, then lo); W2 = B [64 c][r]
+      // up: 64 output columns a step, A operand t (hi and lo, their products apart; P's
+      // columns are free, as t_ready comes after its last run was read); W2 = B [64 c][r]
       // (K-major) forward, A [r][64 c] (MN-major) in the gradient
       const uint32_t id = tc_idesc<XT>(64, false, UP == 1);
       const uint64_t td = tc_desc(t_smem, 16), wd0 = tc_desc(sbase + G::X_BYTES, UP == 0 ? 16 : 8192);
@@ -631,8 +658,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 #pragma unroll
           for (int k = 0; k < RP / 16; ++k)
             if (k < ks)
-              tc_mma(tmem + G::D_COL + 64 * buf, td + (part * G::BLOCKS + k / 4) * (kTcRows * 128 >> 4) + 2 * (k % 4),
-                     UP == 0 ? wd + (k / 4) * 512 + 2 * (k % 4) : wd + 128 * k, id, part > 0 || k > 0);
+              tc_mma(tmem + 128 * buf + 64 * part, td + (part * G::BLOCKS + k / 4) * (kTcRows * 128 >> 4) + 2 * (k % 4),
+                     UP == 0 ? wd + (k / 4) * 512 + 2 * (k % 4) : wd + 128 * k, id, k > 0);
         umma_commit(B.d_full + 8u * buf);
         if (++slot == NS) {
           slot = 0;
