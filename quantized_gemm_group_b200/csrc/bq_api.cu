@@ -1036,7 +1036,9 @@ bq_status launch_wgrad(WgradArgs a, const WgradInputs &in, bool after_dt, cudaSt
   constexpr auto kern = lora_wgrad_kernel<XT, RP>;
   if (!ensure_smem<kern>(G::total)) return BQ_ERR_CUDA;
   // CTAs per cluster: enough to fill the GPU with the adapters that can be in
-  // use; more than that only shortens each CTA's run of rows
+  // use, if they have about as many rows each (the host does not know; with one long
+  // segment beside short ones part of the GPU waits for it); more than that only
+  // shortens each CTA's run of rows
   const int64_t busy = (int64_t)(a.S < a.L ? a.S : a.L) * (a.dA.tiles + a.dB.tiles);
   a.CS = 1;
   while (a.CS < 8 && 2 * busy * a.CS <= (int64_t)sm_count()) a.CS *= 2;

@@ -36,8 +36,8 @@
 //
 // Measured (bf16, each request its own adapter, 4096 columns in): 1 token to
 // 4096 columns, rank 16 5.5 us; 16 requests to 28672, rank 16 14 us and to
-// 14336, rank 64 18 us; 128 requests to 4096, rank 64 29 us (134 MB of pools:
-// 71 % of the copy rate); 256 requests to 14336, rank 64 (64 adapters) 89 us.
+// 14336, rank 64 17 us; 128 requests to 4096, rank 64 29 us (134 MB of pools:
+// 71 % of the copy rate); 256 requests to 14336, rank 64 (64 adapters) 90 us.
 // Few requests are bound by the chain of waits and by the warps' instructions
 // (16 requests: one issued every 2.7 cycles by two warps a scheduler; sixteen
 // warps a CTA were slower, as clusters of 8 then find 15 places instead of 33).
@@ -515,7 +515,7 @@ lora_kernel(LoraArgs a) {
   // first before the sums are exchanged), as a turn is shorter than the way to
   // memory and back.  A lane copies what it reads itself, so no warp waits for
   // another (through registers, B one turn ahead and base none: 16 requests to
-  // 14336 columns, rank 64 23.6 us instead of 18, 1536 rows in 64 segments 48
+  // 14336 columns, rank 64 23.6 us instead of 17, 1536 rows in 64 segments 48
   // instead of 37).  UP = 1 goes through registers: A's columns are transposed
   // on the way.
   constexpr int KC = (RP >= 32) ? RP / 32 : 1;  // runs of 32 ranks (one of 16 where RP = 16)
